@@ -317,3 +317,9 @@ def ssta_forward(desc: Desc, q, k, v, q_text=None, k_text=None, v_text=None, str
     o, o_text = ssta_tile_unorder(desc, op, stream=stream)
     return dict(O=o, O_text=o_text, qp=qp, kp=kp, vp=vp, kv_idx=kv_idx, kv_cnt=kv_cnt, O_packed=op, LSE=lse,
                 ws_mask=ws_mask, ws_attn=ws_attn)
+
+
+from .norm import *  # noqa: E402,F401,F403  (needs the names above)
+from .norm import __all__ as _norm_all  # noqa: E402
+
+__all__ += _norm_all

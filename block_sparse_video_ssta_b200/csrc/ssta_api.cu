@@ -4,8 +4,7 @@
 #include <math.h>
 #include <string.h>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "ssta_api_common.h"
 #include "ssta_internal.h"
 
 namespace ssta {
@@ -13,17 +12,6 @@ namespace {
 
 constexpr int kMaxTileTokens = 4096;   // N; one shared-memory row map per tile
 constexpr int kMaxTiles = 2048;        // NT; one warp holds a score row in registers
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// NVTX range over one library call (host side: validation and kernel enqueue), so a
-// timeline tool shows each call by name; without a tool attached it costs a few ns.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 
 }  // namespace
 
@@ -143,7 +131,7 @@ ssta_status ssta_attention_bwd(const ssta_desc* desc, const void* q_packed, cons
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(int32_t), s) != cudaSuccess) return SSTA_ERR_LAUNCH;
-  return from_cuda(launch_attention_bwd(g, q_packed, k_packed, v_packed, o_packed, lse, do_packed, kv_idx, kv_cnt,
+  return from_cuda(launch_attention_bwd(g, q_packed, k_packed, v_packed, o_packed, nullptr, lse, do_packed, kv_idx, kv_cnt,
                                         dq_packed, dk_packed, dv_packed, workspace, s));
 }
 

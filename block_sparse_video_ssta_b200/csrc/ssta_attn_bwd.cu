@@ -249,8 +249,9 @@ constexpr bool kTensorCores<__nv_bfloat16> = true;
 
 template <typename T>
 cudaError_t launch_bwd_typed(const Geom& g, const void* q, const void* k, const void* v, const void* o,
-                             const float* lse, const void* dO, const int32_t* kv_idx, const int32_t* kv_cnt,
-                             void* dq, void* dk, void* dv, const BwdWorkspace& ws, uint8_t* base, cudaStream_t s) {
+                             const ssta_checkpoint* o_saved, const float* lse, const void* dO, const int32_t* kv_idx,
+                             const int32_t* kv_cnt, void* dq, void* dk, void* dv, const BwdWorkspace& ws, uint8_t* base,
+                             cudaStream_t s) {
   const int64_t rows = (int64_t)g.B * g.H * g.Lq, tiles = (int64_t)g.B * g.H * g.NQ;
   float* Dv = reinterpret_cast<float*>(base + ws.rowdot);
   int32_t* tidx = reinterpret_cast<int32_t*>(base + ws.tidx);
@@ -264,7 +265,7 @@ cudaError_t launch_bwd_typed(const Geom& g, const void* q, const void* k, const 
   float* nl2 = reinterpret_cast<float*>(base + ws.nl2);
   float* nd = reinterpret_cast<float*>(base + ws.nd);
   if constexpr (kTensorCores<T>) {
-    cudaError_t e = launch_attention_bwd_rowstat_tc(g, o, dO, lse, Dv, nl2, nd, s);
+    cudaError_t e = launch_attention_bwd_rowstat_tc(g, o, o_saved, dO, lse, Dv, nl2, nd, s);
     if (e != cudaSuccess) return e;
   } else {
     const int64_t rows_per_block = (int64_t)kBwdWarps * kRowdotRows, BH = (int64_t)g.B * g.H;
@@ -305,14 +306,15 @@ BwdWorkspace bwd_workspace_layout(const Geom& g) {
 }
 
 cudaError_t launch_attention_bwd(const Geom& g, const void* q, const void* k, const void* v, const void* o,
-                                 const float* lse, const void* dO, const int32_t* kv_idx, const int32_t* kv_cnt,
-                                 void* dq, void* dk, void* dv, void* workspace, cudaStream_t s) {
+                                 const ssta_checkpoint* o_saved, const float* lse, const void* dO,
+                                 const int32_t* kv_idx, const int32_t* kv_cnt, void* dq, void* dk, void* dv,
+                                 void* workspace, cudaStream_t s) {
   if ((int64_t)g.B * g.H == 0) return cudaSuccess;
   const BwdWorkspace ws = bwd_workspace_layout(g);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   if (g.dtype == SSTA_BF16)
-    return launch_bwd_typed<__nv_bfloat16>(g, q, k, v, o, lse, dO, kv_idx, kv_cnt, dq, dk, dv, ws, base, s);
-  return launch_bwd_typed<float>(g, q, k, v, o, lse, dO, kv_idx, kv_cnt, dq, dk, dv, ws, base, s);
+    return launch_bwd_typed<__nv_bfloat16>(g, q, k, v, o, o_saved, lse, dO, kv_idx, kv_cnt, dq, dk, dv, ws, base, s);
+  return launch_bwd_typed<float>(g, q, k, v, o, nullptr, lse, dO, kv_idx, kv_cnt, dq, dk, dv, ws, base, s);
 }
 
 }  // namespace ssta

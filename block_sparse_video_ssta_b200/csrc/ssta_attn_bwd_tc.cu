@@ -21,6 +21,7 @@
 // dS(j-1) is written: the next chunk's S and dP run during this chunk's
 // exponentials.  dS is overwritten only after the previous dQ product finished.
 // Every wait is bounded (ssta_wait.cuh), as in the forward kernel.
+#include "ssta_rows.cuh"
 #include "ssta_tc_common.cuh"
 
 #include <algorithm>
@@ -335,16 +336,19 @@ namespace {
 constexpr int kRsWarps = 8;
 constexpr int kRsRows = 8;   // rows per warp
 
+// CODES: O is an 8-bit checkpoint, decoded here (half the bytes of a bf16 O, and no
+// pass that writes its values out).
+template <bool CODES>
 __global__ void __launch_bounds__(kRsWarps * 32)
 bwd_rowstat_tc_kernel(const Geom g, const __grid_constant__ ChunkTables tb, int64_t bh0,
-                      const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO,
-                      const float* __restrict__ lse, float* __restrict__ Dv, float* __restrict__ nl2,
-                      float* __restrict__ nd) {
+                      const __nv_bfloat16* __restrict__ o, const ssta_checkpoint oc,
+                      const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse, float* __restrict__ Dv,
+                      float* __restrict__ nl2, float* __restrict__ nd) {
   const int lane = threadIdx.x & 31, sub = lane >> 4, part = lane & 15;
   const int64_t bh = bh0 + blockIdx.y;
   const int64_t Lp = (int64_t)g.NQ * g.N;
   const int64_t r0 = ((int64_t)blockIdx.x * kRsWarps + (threadIdx.x >> 5)) * kRsRows;
-  int4 va[kRsRows / 2], vb[kRsRows / 2];
+  int4 va[kRsRows / 2], vb[kRsRows / 2];   // CODES: va.x and va.y hold the codes, va.z the exponent byte
   bool valid[kRsRows / 2];
 #pragma unroll
   for (int it = 0; it < kRsRows / 2; ++it) {
@@ -356,19 +360,37 @@ bwd_rowstat_tc_kernel(const Geom g, const __grid_constant__ ChunkTables tb, int6
     }
     valid[it] = ok;
     const int64_t wq = bh * g.Lq + row;
-    va[it] = ok ? reinterpret_cast<const int4*>(o + wq * 128)[part] : make_int4(0, 0, 0, 0);
+    va[it] = make_int4(0, 0, 0, 0);
+    if constexpr (CODES) {
+      if (ok) {
+        const uint2 c = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(oc.codes) + wq * 128)[part];
+        va[it] = make_int4((int)c.x, (int)c.y, oc.exponents[wq], 0);
+      }
+    } else if (ok) {
+      va[it] = reinterpret_cast<const int4*>(o + wq * 128)[part];
+    }
     vb[it] = ok ? reinterpret_cast<const int4*>(dO + wq * 128)[part] : make_int4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int it = 0; it < kRsRows / 2; ++it) {
-    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&va[it]);
     const __nv_bfloat162* y = reinterpret_cast<const __nv_bfloat162*>(&vb[it]);
+    float x[8];
+    if constexpr (CODES) {
+      rows::decode8(make_uint2((uint32_t)va[it].x, (uint32_t)va[it].y), va[it].z, oc.format, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&va[it])[i]);
+        x[2 * i] = u.x;
+        x[2 * i + 1] = u.y;
+      }
+    }
     float d = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 u = __bfloat1622float2(x[i]), v = __bfloat1622float2(y[i]);
-      d = fmaf(u.x, v.x, d);
-      d = fmaf(u.y, v.y, d);
+      const float2 v = __bfloat1622float2(y[i]);
+      d = fmaf(x[2 * i], v.x, d);
+      d = fmaf(x[2 * i + 1], v.y, d);
     }
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
@@ -385,15 +407,21 @@ bwd_rowstat_tc_kernel(const Geom g, const __grid_constant__ ChunkTables tb, int6
 
 }  // namespace
 
-cudaError_t launch_attention_bwd_rowstat_tc(const Geom& g, const void* o, const void* dO, const float* lse, float* Dv,
-                                            float* nl2, float* nd, cudaStream_t s) {
+cudaError_t launch_attention_bwd_rowstat_tc(const Geom& g, const void* o, const ssta_checkpoint* o_saved,
+                                            const void* dO, const float* lse, float* Dv, float* nl2, float* nd,
+                                            cudaStream_t s) {
   const int64_t BH = (int64_t)g.B * g.H;
   const int64_t Lp = (int64_t)g.NQ * g.N, rows_per_block = (int64_t)kRsWarps * kRsRows;
   const ChunkTables tb = make_chunk_tables(g);
   for (int64_t bh0 = 0; bh0 < BH; bh0 += 65535) {   // grid.y holds at most 65535 heads
     const dim3 grid((unsigned)((Lp + rows_per_block - 1) / rows_per_block), (unsigned)std::min<int64_t>(BH - bh0, 65535));
-    bwd_rowstat_tc_kernel<<<grid, kRsWarps * 32, 0, s>>>(g, tb, bh0, static_cast<const __nv_bfloat16*>(o),
-                                                         static_cast<const __nv_bfloat16*>(dO), lse, Dv, nl2, nd);
+    if (o_saved != nullptr)
+      bwd_rowstat_tc_kernel<true><<<grid, kRsWarps * 32, 0, s>>>(g, tb, bh0, nullptr, *o_saved,
+                                                                 static_cast<const __nv_bfloat16*>(dO), lse, Dv, nl2, nd);
+    else
+      bwd_rowstat_tc_kernel<false><<<grid, kRsWarps * 32, 0, s>>>(g, tb, bh0, static_cast<const __nv_bfloat16*>(o),
+                                                                  ssta_checkpoint{}, static_cast<const __nv_bfloat16*>(dO),
+                                                                  lse, Dv, nl2, nd);
   }
   return cudaGetLastError();
 }

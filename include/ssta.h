@@ -251,6 +251,167 @@ ssta_status ssta_build_block_mask_noalloc(const ssta_desc* desc, const void* q_p
                                           int32_t* kv_idx, int32_t* kv_cnt, float* tile_scores, void* stream);
 
 /*
+ * Around the attention: norms, gated residuals and 8-bit checkpoints
+ * -------------------------------------------------------------------
+ * What stands before and after the attention (or the MLP) of a diffusion
+ * transformer block ("HunyuanVideo 1.5 Technical Report", the DiT the attention
+ * runs in), and a way to keep what the backward reads in 8 bits.  These calls
+ * work on rows of C channels: tokens of the residual stream, [rows, C] =
+ * [B * L, H * D], or heads, [B * H * T * Y * X, D].  The conventions above hold
+ * (device pointers, dense storage except the modulation's row stride, alignment,
+ * no allocation, host-checked arguments); none of these calls reports device-side
+ * errors, so they have no status word.
+ *
+ *   norm(x)   layer: (x - mean) * rstd, rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *             rms:   x * rstd,          rstd = 1 / sqrt(mean(x^2) + eps)
+ *             statistics over the C channels of a row, in fp32.
+ *   modulation  scale, shift, gate [G, C]: row i uses modulation row i / mod_rows,
+ *             G = ceil(rows / mod_rows); mod_stride elements lie between two rows,
+ *             so the chunks of one [G, 6 C] tensor serve as they are.
+ *   weights   weight, post_weight [C].
+ * Weights and modulation are of param_dtype; their gradients, and mean and rstd
+ * [rows], are fp32.  A NULL weight counts as 1, a NULL scale or shift as 0, a
+ * NULL gate as 1.
+ */
+typedef enum { SSTA_NORM_NONE = 0, SSTA_NORM_LAYER = 1, SSTA_NORM_RMS = 2 } ssta_norm;
+
+typedef struct {
+  int64_t rows;        /* >= 1 and < 2^31 */
+  int64_t mod_rows;    /* rows sharing one modulation row; 0 = all rows */
+  int64_t mod_stride;  /* elements between modulation rows; 0 = C; a multiple of 8, >= C */
+  int C;               /* channels: a multiple of 8, 8 .. 8192 */
+  int dtype;           /* ssta_dtype of the activations and their gradients */
+  int param_dtype;     /* ssta_dtype of weights and modulation */
+  int norm;            /* ssta_norm before the block (the output y or n) */
+  int post_norm;       /* ssta_norm after the block (of y, before its gate) */
+  float eps;           /* > 0, finite */
+  float res_scale;     /* factor of the residual x, finite */
+} ssta_norm_desc;
+
+typedef struct {
+  int64_t groups;               /* G */
+  int exponents_per_row;        /* ceil(C / 128) */
+  size_t bwd_workspace_bytes;   /* workspace for ssta_norm_bwd and ssta_residual_norm_bwd */
+} ssta_norm_plan_info;
+
+/*
+ * An activation kept in 8 bits.  128 consecutive channels of a row (fewer at its
+ * end) share one exponent byte E: value = code * 2^(E - 127), with E the smallest
+ * in [1, 254] that gives the group's largest magnitude a code.  Codes are rounded
+ * to nearest, ties to even; every value is exact in bf16.  A group that holds an
+ * infinity or a NaN has E = 255 and all its values read as NaN.  Largest error of
+ * a value: max|group| / 127.5 (int8; half a step, and the step is at most twice
+ * the finest one), or |x| * 2^-4 (e4m3; below 2^-14 of the group's largest
+ * magnitude the steps are equal).
+ */
+typedef enum { SSTA_INT8 = 0, SSTA_E4M3 = 1 } ssta_code_format;
+typedef struct {
+  void* codes;         /* [rows, C] one byte each */
+  uint8_t* exponents;  /* [rows, ceil(C / 128)] */
+  int format;          /* ssta_code_format */
+} ssta_checkpoint;
+
+/*
+ * ssta_norm_plan — derive sizes from `desc` (host only, no CUDA call).
+ * SSTA_ERR_INVALID_ARG for malformed descriptors, SSTA_ERR_UNSUPPORTED when C is
+ * no multiple of 8 or above 8192, mod_stride is no multiple of 8, or rows >= 2^31.
+ */
+ssta_status ssta_norm_plan(const ssta_norm_desc* desc, ssta_norm_plan_info* info);
+
+/*
+ * ssta_norm_fwd — the norm before a block, with its modulation:
+ *   y = norm(x) * weight * (1 + scale) + shift.
+ *   x [rows, C] (read), y [rows, C] (written; may be x), mean, rstd [rows]
+ *   (written when non-NULL; mean must be NULL for the RMS norm), x_save (NULL, or
+ *   a checkpoint of x to write in the same pass).
+ * desc->norm must not be SSTA_NORM_NONE; post_norm and res_scale are ignored.
+ */
+ssta_status ssta_norm_fwd(const ssta_norm_desc* desc, const void* x, const void* weight, const void* scale,
+                          const void* shift, void* y, float* mean, float* rstd, const ssta_checkpoint* x_save,
+                          void* stream);
+
+/*
+ * ssta_norm_bwd — gradients of ssta_norm_fwd.  With xh = norm(x) from the saved
+ * statistics and g = dy * weight * (1 + scale):
+ *   dx = dres + rstd * (g - mean(g) - xh * mean(g * xh))   (rms: without mean(g))
+ *   dshift = sum dy, dscale = sum dy * xh * weight   over the rows of each group
+ *   dweight = sum dy * (1 + scale) * xh              over all rows
+ *   dy [rows, C] (read), x [rows, C] or x_saved (exactly one non-NULL; read),
+ *   mean (layer norm), rstd (read), dres [rows, C] (read when non-NULL: the
+ *   gradient that reaches x past the block), dx [rows, C] (written; may be dy or
+ *   dres), dweight [C], dscale, dshift [G, C] dense fp32 (written when non-NULL),
+ *   workspace >= info.bwd_workspace_bytes (contents overwritten).
+ * Sums run in a fixed order: equal inputs give equal bytes.
+ */
+ssta_status ssta_norm_bwd(const ssta_norm_desc* desc, const void* dy, const void* x, const ssta_checkpoint* x_saved,
+                          const float* mean, const float* rstd, const void* weight, const void* scale,
+                          const void* dres, void* dx, float* dweight, float* dscale, float* dshift, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * ssta_residual_norm_fwd — behind a block whose output is y: the residual with the
+ * block's gate, and the norm before the next block, in one pass:
+ *   h = post_norm(y) * post_weight   (post_norm none: h = y)
+ *   r = res_scale * x + gate * h
+ *   n = norm(r) * weight * (1 + scale) + shift   (norm none: n is not written)
+ *   x, y [rows, C] (read), r [rows, C] (written; may be x), n [rows, C] (written;
+ *   may be y; NULL iff norm is none), post_mean, post_rstd, mean, rstd [rows]
+ *   (written when non-NULL; each must be NULL where its norm has none), y_save,
+ *   r_save (NULL, or checkpoints of y and of the stored r to write in the same
+ *   pass).  n and the statistics are those of r before it is rounded to dtype.
+ */
+ssta_status ssta_residual_norm_fwd(const ssta_norm_desc* desc, const void* x, const void* y, const void* post_weight,
+                                   const void* gate, const void* weight, const void* scale, const void* shift,
+                                   void* r, void* n, float* post_mean, float* post_rstd, float* mean, float* rstd,
+                                   const ssta_checkpoint* y_save, const ssta_checkpoint* r_save, void* stream);
+
+/*
+ * ssta_residual_norm_bwd — gradients of ssta_residual_norm_fwd, from dr and dn, the
+ * gradients of r and n (either may be NULL, not both; dn must be NULL when norm is
+ * none).  With rh = norm(r), yh = post_norm(y) (none: y), g = dn * weight * (1 + scale):
+ *   dR = dr + rstd * (g - mean(g) - rh * mean(g * rh)),  dx = res_scale * dR
+ *   dh = dR * gate * post_weight,  dy = dh, or its gradient through post_norm
+ *   dgate = sum dR * yh * post_weight, dshift, dscale as above   over each group
+ *   dpost_weight = sum dR * gate * yh, dweight as above          over all rows
+ *   r or r_saved (needed with dn), y or y_saved (needed for post_norm, dgate and
+ *   dpost_weight): at most one of each pair, and where both r and y are given, both
+ *   dense or both checkpoints of one format.  dx, dy [rows, C] (written; dx may be
+ *   dr, dy may be dn), gradients of the vectors written when non-NULL
+ *   (dpost_weight needs a post_norm; dweight, dscale, dshift need dn).
+ */
+ssta_status ssta_residual_norm_bwd(const ssta_norm_desc* desc, const void* dr, const void* dn, const void* r,
+                                   const ssta_checkpoint* r_saved, const void* y, const ssta_checkpoint* y_saved,
+                                   const float* post_mean, const float* post_rstd, const float* mean,
+                                   const float* rstd, const void* post_weight, const void* gate, const void* weight,
+                                   const void* scale, void* dx, void* dy, float* dpost_weight, float* dgate,
+                                   float* dweight, float* dscale, float* dshift, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * ssta_checkpoint_save — write the checkpoint of x [rows, C] (dtype, read).
+ * ssta_checkpoint_load — write the values of a checkpoint to x [rows, C] (dtype).
+ * rows >= 1, C >= 8 and a multiple of 8, at most 2^36 groups (rows * ceil(C / 128)).
+ */
+ssta_status ssta_checkpoint_save(int64_t rows, int C, int dtype, const void* x, const ssta_checkpoint* out,
+                                 void* stream);
+ssta_status ssta_checkpoint_load(int64_t rows, int C, int dtype, const ssta_checkpoint* in, void* x, void* stream);
+
+/*
+ * ssta_attention_bwd_checkpoint — ssta_attention_bwd with q, k, v and O kept in 8
+ * bits: checkpoints of the packed tensors ([B*H*Lq, 128], one format for all
+ * four).  The formulas of ssta_attention_bwd at the checkpoints' values; lse is the
+ * forward's.  workspace >= ssta_attention_bwd_checkpoint_workspace (which is
+ * info.bwd_workspace_bytes and room for the values of q, k and v; status word
+ * first).  Otherwise as ssta_attention_bwd.
+ */
+ssta_status ssta_attention_bwd_checkpoint_workspace(const ssta_desc* desc, size_t* bytes);
+ssta_status ssta_attention_bwd_checkpoint(const ssta_desc* desc, const ssta_checkpoint* q, const ssta_checkpoint* k,
+                                          const ssta_checkpoint* v, const ssta_checkpoint* o, const float* lse,
+                                          const void* do_packed, const int32_t* kv_idx, const int32_t* kv_cnt,
+                                          void* dq_packed, void* dk_packed, void* dv_packed, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/*
  * ssta_selftest_bounded_wait — runs the device-side bounded wait that guards every
  * pipeline wait of ssta_attention_fwd on a barrier phase that never completes
  * (complete == 0) or that completes at once (complete != 0).  The paper has no
