@@ -8,8 +8,9 @@
 // so a code is the nearest one to x with ties to even and nothing else is rounded, and a
 // code times its scale (7 or 4 significant bits) is exact in bf16: what the tensor cores
 // multiply is what the checkpoint holds.  A finer scale would halve int8's step at most
-// and put a rounding behind every read.  A group with an infinity or a NaN gets E = 255
-// and reads as NaN throughout, so an overflow stays visible in the gradients.
+// and put a rounding behind every read.  A group with an infinity, a NaN or a magnitude
+// whose nearest value would be 2^128 gets E = 255 and reads as NaN throughout, so an
+// overflow stays visible in the gradients.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -82,7 +83,8 @@ __device__ __forceinline__ void load_param8(const void* p, int64_t i, bool is_f3
 
 // Exponent byte of a group from the bits of its largest magnitude.
 __device__ __forceinline__ int group_exponent(uint32_t amax, int format) {
-  if (amax >= 0x7f800000u) return 255;
+  // from 63.75 * 2^122 (int8) or 248 * 2^120 (e4m3) on, the nearest value is 2^128
+  if (amax >= (format == SSTA_INT8 ? 0x7f7f0000u : 0x7f780000u)) return 255;
   const int f = (int)(amax >> 23);
   const uint32_t m = amax & 0x7fffffu;
   // 127.5 = 1.9921875 * 2^6 (not reached), 448 = 1.75 * 2^8 (reached)

@@ -98,7 +98,7 @@ def ssta_norm_plan(desc: NormDesc) -> NormPlan:
 class Checkpoint:
     """An activation kept in 8 bits: ``codes`` [..., C] (torch.int8 or torch.float8_e4m3fn), ``exponents``
     [..., ceil(C / 128)] (torch.uint8), and the ``dtype`` its values are read as.  The value of a code is
-    code * 2^(exponent - 127); exponent 255 marks a group that held an infinity or a NaN."""
+    code * 2^(exponent - 127); exponent 255 marks a group that held an infinity or a NaN (its values read as NaN)."""
     __slots__ = ("codes", "exponents", "dtype", "_c")
 
     def __init__(self, codes, exponents, dtype=torch.bfloat16):

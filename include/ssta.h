@@ -299,7 +299,8 @@ typedef struct {
  * end) share one exponent byte E: value = code * 2^(E - 127), with E the smallest
  * in [1, 254] that gives the group's largest magnitude a code.  Codes are rounded
  * to nearest, ties to even; every value is exact in bf16.  A group that holds an
- * infinity or a NaN has E = 255 and all its values read as NaN.  Largest error of
+ * infinity, a NaN or a magnitude whose nearest value would be 2^128 has E = 255 and
+ * all its values read as NaN.  Largest error of
  * a value: max|group| / 127.5 (int8; half a step, and the step is at most twice
  * the finest one), or |x| * 2^-4 (e4m3; below 2^-14 of the group's largest
  * magnitude the steps are equal).
