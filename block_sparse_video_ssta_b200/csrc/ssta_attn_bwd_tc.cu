@@ -376,7 +376,10 @@ bwd_rowstat_tc_kernel(const Geom g, const __grid_constant__ ChunkTables tb, int6
     const __nv_bfloat162* y = reinterpret_cast<const __nv_bfloat162*>(&vb[it]);
     float x[8];
     if constexpr (CODES) {
-      rows::decode8(make_uint2((uint32_t)va[it].x, (uint32_t)va[it].y), va[it].z, oc.format, x);
+      const rows::V8 c = rows::mul(rows::decode8(make_uint2((uint32_t)va[it].x, (uint32_t)va[it].y), oc.format),
+                                   rows::code_scale(va[it].z));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows::f2_unpack(c.p[i], x[2 * i], x[2 * i + 1]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -44,8 +44,7 @@ __global__ void __launch_bounds__(kThreads) checkpoint_save_kernel(const __grid_
   }
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
-    float v[kVec];
-    unpack(raw[i], v);
+    const V8 v = unpack(raw[i]);
     const int E = group_exponent(group_amax(v), p.format);
     if (off[i] >= 0) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out[0]) + off[i]) = encode8(v, E, p.format);
@@ -75,9 +74,7 @@ __global__ void __launch_bounds__(kThreads) checkpoint_load_kernel(const __grid_
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (off[i] < 0) continue;
-    float v[kVec];
-    decode8(c[i], E[i], p.format, v);
-    store8(out + off[i], v);
+    store8(out + off[i], mul(decode8(c[i], p.format), code_scale(E[i])));
   }
 }
 

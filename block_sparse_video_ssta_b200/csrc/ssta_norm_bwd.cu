@@ -11,10 +11,16 @@
 // throughout: its share of S1-S3 and the products of the vectors stay in registers, and
 // the sums leave the SM once per run instead of once per row.  The rows ahead come by
 // cp.async into slots of shared memory that only the copying thread reads: several rows
-// are in flight per thread without registers and without a barrier.  r and y may be 8-bit
-// checkpoints: their codes are what is copied, and they are decoded on the way to
-// registers, which saves one of the two bytes of a bf16 read.  Two small kernels add the
-// runs' sums in a fixed order (no atomics: equal inputs give equal bytes).
+// are in flight per thread without registers and without a barrier (channels and rows
+// that do not exist are filled with zeros there, so the arithmetic has no conditions).
+// r and y may be 8-bit checkpoints: their codes are what is copied, and they are decoded
+// on the way to registers, which saves one of the two bytes of a bf16 read.  Two small
+// kernels add the runs' sums in a fixed order (no atomics: equal inputs give equal bytes).
+//
+// What bounds it: HBM, once the instructions fit.  A thread handles two rows at a time
+// (bf16) and works on pairs of channels; the row sums of both rows share one butterfly,
+// in which a lane gives away the sums that it need not finish (6 shuffles for four sums
+// instead of 20).
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
 
@@ -41,8 +47,8 @@ struct BwdParams {
   bool param_f32;
 };
 
-// Threads of a row, rows at a time and runs per group; the same for every type, so that
-// the workspace follows from the descriptor.
+// Threads of a row, rows at once (slots; each takes U at a time) and runs per group; the
+// same for every type, so that the workspace follows from the descriptor.
 struct BwdShape {
   int row_threads, slots, chunks;
   uint32_t chunk_rows;
@@ -54,7 +60,8 @@ BwdShape bwd_shape(const NormGeom& g) {
     b.row_threads = 16;
     b.slots = 16;
   } else {
-    b.row_threads = (g.C / kVec + 31) / 32 * 32;
+    const int vecs = g.C <= 4096 ? g.C / kVec : (g.C / kVec + 1) / 2;   // above, two vectors per thread
+    b.row_threads = (vecs + 31) / 32 * 32;
     b.slots = std::max(1, 256 / b.row_threads);
   }
   // Runs per group: as many blocks as the SMs hold at once (or a small multiple, whichever
@@ -77,277 +84,346 @@ BwdShape bwd_shape(const NormGeom& g) {
   return b;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Copies to shared memory; zeros instead where `live` is false (the address is not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // A thread's slot for one vector of a dense tensor: 16-byte planes, one entry per thread
 // in each (neighbouring threads' 16 bytes are neighbours, no bank conflicts).
-template <typename T> constexpr int kPlanes = (int)sizeof(T) * kVec / 16;
-template <typename T> __device__ __forceinline__ void copy_dense(uint32_t slot, int threads, const T* src) {
-#pragma unroll
-  for (int i = 0; i < kPlanes<T>; ++i) cp_async16(slot + (i * threads + threadIdx.x) * 16, reinterpret_cast<const char*>(src) + 16 * i);
+template <int MAXT>
+__device__ __forceinline__ void copy_dense(uint32_t slot, const __nv_bfloat16* src, bool live) {
+  cp_async16(slot + threadIdx.x * 16, src, live);
 }
-__device__ __forceinline__ Raw<__nv_bfloat16> read_dense(const uint8_t* slot, int, __nv_bfloat16) {
-  return {reinterpret_cast<const uint4*>(slot)[threadIdx.x]};
+template <int MAXT>
+__device__ __forceinline__ void copy_dense(uint32_t slot, const float* src, bool live) {
+  cp_async16(slot + threadIdx.x * 16, src, live);
+  cp_async16(slot + (MAXT + threadIdx.x) * 16, src + 4, live);
 }
-__device__ __forceinline__ Raw<float> read_dense(const uint8_t* slot, int threads, float) {
-  return {reinterpret_cast<const float4*>(slot)[threadIdx.x], reinterpret_cast<const float4*>(slot)[threads + threadIdx.x]};
+template <int MAXT>
+__device__ __forceinline__ V8 read_dense(const uint8_t* slot, __nv_bfloat16) {
+  return unpack(Raw<__nv_bfloat16>{reinterpret_cast<const uint4*>(slot)[threadIdx.x]});
+}
+template <int MAXT>
+__device__ __forceinline__ V8 read_dense(const uint8_t* slot, float) {
+  return unpack(Raw<float>{reinterpret_cast<const float4*>(slot)[threadIdx.x],
+                           reinterpret_cast<const float4*>(slot)[MAXT + threadIdx.x]});
 }
 
-// The sums of a and b over the threads of a row.  HALF: a row is half a warp.
-template <bool HALF>
-__device__ __forceinline__ void row_sum2(float& a, float& b, const BwdParams& p, float2* exchange, int slot) {
-#pragma unroll
-  for (int off = HALF ? 8 : 16; off > 0; off >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, off);
-    b += __shfl_xor_sync(0xffffffffu, b, off);
+// Sums of a[u] and b[u] over the threads of each of U rows (1 or 2); every thread of the
+// rows gets them.  A row is a half-warp (HALF) or `warps` warps.  In the first steps a lane
+// keeps half of its sums and hands the others to its partner, so each sum ends in a part
+// of the lanes, from which the warps' parts are added and handed round.
+template <bool HALF, int U>
+__device__ __forceinline__ void row_sums(float (&a)[U], float (&b)[U], int warps, float* exchange, int slot) {
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int kLanes = HALF ? 16 : 32;
+  const int lane = threadIdx.x & 31;
+  int off = kLanes / 2;
+  float x, y;
+  if constexpr (U == 2) {
+    const bool up = lane & off;
+    x = (up ? a[1] : a[0]) + __shfl_xor_sync(kAll, up ? a[0] : a[1], off);
+    y = (up ? b[1] : b[0]) + __shfl_xor_sync(kAll, up ? b[0] : b[1], off);
+    off /= 2;
+  } else {
+    x = a[0];
+    y = b[0];
   }
+  const bool up = lane & off;
+  float v = (up ? y : x) + __shfl_xor_sync(kAll, up ? x : y, off);
+  const int part = off;   // lanes holding one sum: its index is the lane over `part`
+#pragma unroll
+  for (off /= 2; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  const int first = lane & ~(kLanes - 1);
   if constexpr (!HALF) {
-    const int warps = p.row_threads >> 5;
     if (warps > 1) {
-      if ((threadIdx.x & 31) == 0) exchange[threadIdx.x >> 5] = make_float2(a, b);
-      asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(p.row_threads) : "memory");
-      a = b = 0.f;
-      for (int w = 0; w < warps; ++w) {
-        const float2 e = exchange[slot * warps + w];
-        a += e.x;
-        b += e.y;
-      }
+      float* row = exchange + slot * warps * (2 * U);
+      if (lane % part == 0) row[(lane / part) * warps + ((threadIdx.x >> 5) - slot * warps)] = v;
+      asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(warps * 32) : "memory");
+      v = 0.f;
+      for (int w = lane % part; w < warps; w += part) v += row[(lane / part) * warps + w];
+#pragma unroll
+      for (int o = part / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     }
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    a[u] = __shfl_sync(kAll, v, first + 2 * u * part);
+    b[u] = __shfl_sync(kAll, v, first + (2 * u + 1) * part);
+  }
 }
 
-template <typename T, bool CODES, bool POST, bool HALF, int MAXT>
-struct Kernel {
-  // bytes of a thread's slots per row: dn, dr, r and (behind a gated residual) y
-  static constexpr int kDense = (int)sizeof(T) * kVec, kKept = CODES ? 8 : kDense;
-  static constexpr int kRowBytes = 2 * kDense + (POST ? 2 : 1) * kKept;
-  // rows in flight: four where two blocks still share an SM, fewer for the widest rows
-  static constexpr int kFit = (MAXT <= 256 ? 110 : 200) * 1024 / (MAXT * kRowBytes);
-  static constexpr int kStages = kFit < 1 ? 1 : kFit < 4 ? kFit : 4;
-  static constexpr int kSmem = (kStages * kRowBytes > kSums * kVec * 4 ? kStages * kRowBytes : kSums * kVec * 4) * MAXT;
+// What a row brings besides its channels, in shared memory for kWindow rows at a time:
+// xh = v * scale + shift of both norms, and the checkpoints' exponent bytes.
+constexpr int kWindow = 64;   // a multiple of the rows a block takes at once (at most 32)
+struct RowScalars {
+  float rstd, shift, prstd, pshift;
 };
 
-template <typename T, bool CODES, bool POST, bool HALF, int MAXT>
+// SRC: 0 dense r and y, 1 + format: checkpoints.
+template <typename T, int SRC, bool POST, bool HALF, int NV, int U, int MAXT>
+struct Kernel {
+  // bytes of a thread's slots per vector: dn, dr, r and (behind a gated residual) y
+  static constexpr int kDense = (int)sizeof(T) * kVec, kKept = SRC ? 8 : kDense;
+  static constexpr int kVecBytes = 2 * kDense + (POST ? 2 : 1) * kKept;
+  static constexpr int kStageBytes = NV * U * kVecBytes * MAXT;
+  static constexpr int kExps = SRC ? MAXT * NV * kVec / kGroup : 0;   // exponent bytes of a row
+  static constexpr int kTable = kWindow * ((int)sizeof(RowScalars) + (POST ? 2 : 1) * kExps);
+  // copies in flight: up to four times U rows, as far as shared memory goes (two blocks of
+  // 256 threads, or one larger one, per SM)
+  static constexpr int kFit = ((MAXT <= 256 ? 112 : 224) * 1024 - kTable) / kStageBytes;
+  static constexpr int kStages = kFit < 1 ? 1 : kFit < 4 ? kFit : 4;
+  static constexpr int kSumBytes = kSums * NV * kVec * 4 * MAXT;
+  static constexpr int kSmem = kTable + (kStages * kStageBytes > kSumBytes ? kStages * kStageBytes : kSumBytes);
+};
+
+template <typename T, int SRC, bool POST, bool HALF, int NV, int U, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ BwdParams p) {
-  using K = Kernel<T, CODES, POST, HALF, MAXT>;
-  extern __shared__ __align__(16) uint8_t stage[];
-  __shared__ float2 exchange[2][2][MAXT / 32];
+  using K = Kernel<T, SRC, POST, HALF, NV, U, MAXT>;
+  constexpr int kFormat = SRC - 1;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float exchange[2][2][2 * U * (MAXT / 32)];
+  RowScalars* const table = reinterpret_cast<RowScalars*>(smem);
+  uint8_t* const exps_r = smem + kWindow * sizeof(RowScalars);
+  uint8_t* const exps_y = exps_r + kWindow * K::kExps;
+  uint8_t* const stage = smem + K::kTable;
   const NormBwdArgs& a = p.a;
-  const int threads = blockDim.x;
+  const int warps = p.row_threads >> 5;
   const int slot = HALF ? threadIdx.x >> 4 : threadIdx.x / p.row_threads;
   const int lane = HALF ? threadIdx.x & 15 : threadIdx.x % p.row_threads;
-  const int ch = lane * kVec;
-  const bool in = ch < p.C;
+  const int step = p.row_threads * kVec;   // between a thread's vectors
   const uint32_t item = blockIdx.x, grp = item / p.chunks, chunk = item % p.chunks;
-  const int64_t first = (int64_t)grp * p.mod_rows + (int64_t)chunk * p.chunk_rows;
-  const int64_t group_end = min((int64_t)(grp + 1) * p.mod_rows, (int64_t)p.rows);
-  const int64_t last = min(first + p.chunk_rows, group_end);
-  const int iters = last > first ? (int)((last - first + p.slots - 1) / p.slots) : 0;
+  const int64_t group_first = (int64_t)grp * p.mod_rows;
+  const int64_t first = group_first + (int64_t)chunk * p.chunk_rows;
+  const int64_t group_end = min(group_first + p.mod_rows, (int64_t)p.rows);
+  const int count = (int)max(min((int64_t)p.chunk_rows, group_end - first), (int64_t)0);   // rows of this run
+  const int per_iter = p.slots * U;
   const bool has_n = a.dn != nullptr, has_r = a.dr != nullptr;
   const bool has_y = POST && (a.y != nullptr || a.y_saved.codes != nullptr);
+  bool in[NV];   // this vector's channels exist
+#pragma unroll
+  for (int i = 0; i < NV; ++i) in[i] = lane * kVec + i * step < p.C;
 
   const uint32_t stage0 = (uint32_t)__cvta_generic_to_shared(stage);
-  auto prefetch = [&](int it) {
-    const int64_t row = first + (int64_t)it * p.slots + slot;
-    if (in && it < iters && row < last) {
-      const int64_t at = row * p.C + ch;
-      uint32_t s = stage0 + (it % K::kStages) * K::kRowBytes * threads;
-      if (has_n) copy_dense(s, threads, static_cast<const T*>(a.dn) + at);
-      s += K::kDense * threads;
-      if (has_r) copy_dense(s, threads, static_cast<const T*>(a.dr) + at);
-      s += K::kDense * threads;
-      if (has_n) {
-        if constexpr (CODES) cp_async8(s + threadIdx.x * 8, static_cast<const uint8_t*>(a.r_saved.codes) + at);
-        else copy_dense(s, threads, static_cast<const T*>(a.r) + at);
-      }
-      if constexpr (POST) {
-        s += K::kKept * threads;
-        if (has_y) {
-          if constexpr (CODES) cp_async8(s + threadIdx.x * 8, static_cast<const uint8_t*>(a.y_saved.codes) + at);
-          else copy_dense(s, threads, static_cast<const T*>(a.y) + at);
+  const int64_t at0 = first * p.C + lane * kVec;   // this thread's first channel in row `first`
+  auto prefetch = [&](int r0, int st) {   // rows r0 .. of this thread's slot into stage st
+    const uint32_t base = stage0 + st * K::kStageBytes;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row_at = r0 + u < count ? at0 + (int64_t)(r0 + u) * p.C : at0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool live = r0 + u < count && in[i];
+        const int64_t at = live ? row_at + i * step : 0;
+        const uint32_t s = base + (u * NV + i) * (K::kVecBytes * MAXT);
+        if (has_n) {
+          copy_dense<MAXT>(s, static_cast<const T*>(a.dn) + at, live);
+          if constexpr (SRC) cp_async8(s + 2 * K::kDense * MAXT + threadIdx.x * 8, static_cast<const uint8_t*>(a.r_saved.codes) + at, live);
+          else copy_dense<MAXT>(s + 2 * K::kDense * MAXT, static_cast<const T*>(a.r) + at, live);
+        }
+        if (has_r) copy_dense<MAXT>(s + K::kDense * MAXT, static_cast<const T*>(a.dr) + at, live);
+        if constexpr (POST) {
+          constexpr int kY = (2 * K::kDense + K::kKept) * MAXT;
+          if (has_y) {
+            if constexpr (SRC) cp_async8(s + kY + threadIdx.x * 8, static_cast<const uint8_t*>(a.y_saved.codes) + at, live);
+            else copy_dense<MAXT>(s + kY, static_cast<const T*>(a.y) + at, live);
+          }
         }
       }
     }
     cp_commit();
   };
-  // a row's scalars, fetched one row ahead into registers
-  struct Scalars { float mean, rstd, pmean, prstd; int er, ey; };
-  auto scalars = [&](int it) {
-    Scalars v{0.f, 0.f, 0.f, 1.f, 1, 1};
-    const int64_t row = first + (int64_t)it * p.slots + slot;
-    if (in && it < iters && row < last) {
-      if (has_n) {
-        v.rstd = a.rstd[row];
-        if (p.norm == SSTA_NORM_LAYER) v.mean = a.mean[row];
-        if constexpr (CODES) v.er = a.r_saved.exponents[row * p.groups_per_row + ch / kGroup];
+  // Fills the table for the kWindow rows from w0 on (a row that does not exist has rstd 0
+  // and readable exponents).
+  auto fill_table = [&](int w0) {
+    __syncthreads();
+    for (int r = threadIdx.x; r < kWindow; r += blockDim.x) {
+      RowScalars v{0.f, 0.f, 1.f, 0.f};
+      if (w0 + r < count) {
+        const int64_t row = first + w0 + r;
+        if (has_n) {
+          v.rstd = a.rstd[row];
+          if (p.norm == SSTA_NORM_LAYER) v.shift = -a.mean[row] * v.rstd;
+        }
+        if constexpr (POST) {
+          if (p.post_norm != SSTA_NORM_NONE) v.prstd = a.post_rstd[row];
+          if (p.post_norm == SSTA_NORM_LAYER) v.pshift = -a.post_mean[row] * v.prstd;
+        }
       }
-      if constexpr (POST) {
-        if (p.post_norm != SSTA_NORM_NONE) v.prstd = a.post_rstd[row];
-        if (p.post_norm == SSTA_NORM_LAYER) v.pmean = a.post_mean[row];
-        if constexpr (CODES) {
-          if (has_y) v.ey = a.y_saved.exponents[row * p.groups_per_row + ch / kGroup];
+      table[r] = v;
+    }
+    if constexpr (SRC) {
+      const int64_t from = (first + w0) * p.groups_per_row;
+      const int n = min(kWindow, count - w0) * p.groups_per_row;
+      for (int e = threadIdx.x; e < kWindow * p.groups_per_row; e += blockDim.x) {
+        if (has_n) exps_r[e] = e < n ? a.r_saved.exponents[from + e] : 1;
+        if constexpr (POST) {
+          if (has_y) exps_y[e] = e < n ? a.y_saved.exponents[from + e] : 1;
         }
       }
     }
-    return v;
+    __syncthreads();
   };
 
+  int r0 = slot * U;
 #pragma unroll
-  for (int i = 0; i < K::kStages; ++i) prefetch(i);
-  Scalars next = scalars(0);
+  for (int i = 0; i < K::kStages; ++i) prefetch(r0 + i * per_iter, i);
 
-  // products of the vectors for this thread's channels
-  float gw[kVec], gp[kVec];
+  // products of the vectors for this thread's channels (0 beyond C)
+  V8 gw[NV], gp[POST ? NV : 1];
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) gw[j] = gp[j] = 1.f;
-  if (in) {
+  for (int i = 0; i < NV; ++i) {
+    const int ch = lane * kVec + i * step;
     const int64_t mod = (int64_t)grp * p.mod_stride + ch;
-    float w[kVec];
-    if (a.weight != nullptr) {
-      load_param8(a.weight, ch, p.param_f32, w);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) gw[j] = w[j];
-    }
-    if (a.scale != nullptr) {
-      load_param8(a.scale, mod, p.param_f32, w);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) gw[j] *= 1.f + w[j];
-    }
+    gw[i] = fill(in[i] ? 1.f : 0.f);
+    if (in[i] && a.weight != nullptr) gw[i] = load_param8(a.weight, ch, p.param_f32);
+    if (in[i] && a.scale != nullptr) gw[i] = mul(gw[i], add(load_param8(a.scale, mod, p.param_f32), fill(1.f)));
     if constexpr (POST) {
-      if (a.post_weight != nullptr) {
-        load_param8(a.post_weight, ch, p.param_f32, w);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) gp[j] = w[j];
-      }
-      if (a.gate != nullptr) {
-        load_param8(a.gate, mod, p.param_f32, w);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) gp[j] *= w[j];
-      }
+      gp[i] = fill(in[i] ? 1.f : 0.f);
+      if (in[i] && a.post_weight != nullptr) gp[i] = load_param8(a.post_weight, ch, p.param_f32);
+      if (in[i] && a.gate != nullptr) gp[i] = mul(gp[i], load_param8(a.gate, mod, p.param_f32));
     }
   }
-  float s1[kVec], s2[kVec], s3[kVec];
+  V8 s1[NV], s2[NV], s3[POST ? NV : 1];
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) s1[j] = s2[j] = s3[j] = 0.f;
+  for (int i = 0; i < NV; ++i) s1[i] = s2[i] = fill(0.f);
+  if constexpr (POST) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s3[i] = fill(0.f);
+  }
 
-  for (int it = 0; it < iters; ++it) {
-    const Scalars sc = next;
-    next = scalars(it + 1);
+  int st = 0, parity = 0;
+  for (int done = 0; done < count; done += per_iter, r0 += per_iter) {
+    if (done % kWindow == 0) fill_table(done);
     cp_wait<K::kStages - 1>();
-    const int64_t row = first + (int64_t)it * p.slots + slot;
-    const bool alive = in && row < last;   // others carry zeros through the sums
-    const uint8_t* s = stage + (it % K::kStages) * K::kRowBytes * threads;
-    float dR[kVec], yh[POST ? kVec : 1];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) dR[j] = 0.f;
-    if (has_r && alive) unpack(read_dense(s + K::kDense * threads, threads, T()), dR);
+    const uint8_t* const s = stage + st * K::kStageBytes;
+    const int wr = r0 % kWindow;
+    auto place = [&](int u, int i, int offset) { return s + ((u * NV + i) * K::kVecBytes + offset) * MAXT; };
+    auto kept = [&](int u, int i, int offset, const uint8_t* exps, float scale, float shift) {
+      if constexpr (SRC) {
+        const int E = exps[(wr + u) * p.groups_per_row + (in[i] ? (lane * kVec + i * step) / kGroup : 0)];
+        return fma(decode8(reinterpret_cast<const uint2*>(place(u, i, offset))[threadIdx.x], kFormat),
+                   code_scale(E) * scale, shift);
+      } else {
+        return fma(read_dense<MAXT>(place(u, i, offset), T()), scale, shift);
+      }
+    };
+    V8 g[U][NV], rh[U][NV];
+    float m1[U], m2[U];
     if (has_n) {
-      float dn[kVec], rh[kVec];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) dn[j] = rh[j] = 0.f;
-      if (alive) {
-        unpack(read_dense(s, threads, T()), dn);
-        const uint8_t* sr = s + 2 * K::kDense * threads;
-        if constexpr (CODES) decode8(reinterpret_cast<const uint2*>(sr)[threadIdx.x], sc.er, p.format, rh);
-        else unpack(read_dense(sr, threads, T()), rh);
+      for (int u = 0; u < U; ++u) {
+        const float2 rs = *reinterpret_cast<const float2*>(&table[wr + u].rstd);
+        m1[u] = m2[u] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) rh[j] = (rh[j] - sc.mean) * sc.rstd;
-      }
-      float m1 = 0.f, m2 = 0.f;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        s1[j] += dn[j];
-        s2[j] = fmaf(dn[j], rh[j], s2[j]);
-        dn[j] *= gw[j];
-        m1 += dn[j];
-        m2 = fmaf(dn[j], rh[j], m2);
-      }
-      row_sum2<HALF>(m1, m2, p, exchange[it & 1][0], slot);
-      m1 = p.norm == SSTA_NORM_LAYER ? m1 * p.inv_c : 0.f;
-      m2 *= p.inv_c;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) dR[j] = fmaf(sc.rstd, dn[j] - m1 - rh[j] * m2, dR[j]);
-    }
-    if (alive) {
-      float out[kVec];
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) out[j] = POST ? p.res_scale * dR[j] : dR[j];
-      store8(static_cast<T*>(a.dx) + row * p.C + ch, out);
-    }
-    if constexpr (POST) {
-      if (has_y) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) yh[j] = 0.f;
-        if (alive) {
-          const uint8_t* sy = s + (2 * K::kDense + K::kKept) * threads;
-          if constexpr (CODES) decode8(reinterpret_cast<const uint2*>(sy)[threadIdx.x], sc.ey, p.format, yh);
-          else unpack(read_dense(sy, threads, T()), yh);
-        }
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          if (p.post_norm != SSTA_NORM_NONE) yh[j] = alive ? (yh[j] - sc.pmean) * sc.prstd : 0.f;
-          s3[j] = fmaf(dR[j], yh[j], s3[j]);
+        for (int i = 0; i < NV; ++i) {
+          const V8 dn = read_dense<MAXT>(place(u, i, 0), T());
+          rh[u][i] = kept(u, i, 2 * K::kDense, exps_r, rs.x, rs.y);
+          s1[i] = add(s1[i], dn);
+          s2[i] = fma(dn, rh[u][i], s2[i]);
+          g[u][i] = mul(dn, gw[i]);
+          m1[u] += sum(g[u][i]);
+          m2[u] += dot(g[u][i], rh[u][i]);
         }
       }
+      row_sums<HALF, U>(m1, m2, warps, exchange[parity][0], slot);
+    }
+    V8 dR[U][NV], yh[POST ? U : 1][POST ? NV : 1];
+    float q1[U], q2[U];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) dR[j] *= gp[j];
-      if (p.post_norm != SSTA_NORM_NONE) {
-        float m1 = 0.f, m2 = 0.f;
-        if (alive) {   // dR holds the norm's row terms also where no channel is
+    for (int u = 0; u < U; ++u) {
+      q1[u] = q2[u] = 0.f;
+      const RowScalars sc = table[wr + u];
+      const float c1 = has_n && p.norm == SSTA_NORM_LAYER ? -sc.rstd * (m1[u] * p.inv_c) : 0.f;
+      const float c2 = has_n ? -sc.rstd * (m2[u] * p.inv_c) : 0.f;
+      const int64_t row_at = at0 + (int64_t)(r0 + u) * p.C;
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            m1 += dR[j];
-            m2 = fmaf(dR[j], yh[j], m2);
+      for (int i = 0; i < NV; ++i) {
+        dR[u][i] = has_r ? read_dense<MAXT>(place(u, i, K::kDense), T()) : fill(0.f);
+        if (has_n) dR[u][i] = add(dR[u][i], fma(sc.rstd, g[u][i], fma(rh[u][i], c2, c1)));
+        const bool alive = r0 + u < count && in[i];
+        if (alive) store8(static_cast<T*>(a.dx) + row_at + i * step, POST ? mul(dR[u][i], p.res_scale) : dR[u][i]);
+        if constexpr (POST) {
+          if (has_y) {
+            yh[u][i] = kept(u, i, 2 * K::kDense + K::kKept, exps_y, sc.prstd, sc.pshift);
+            s3[i] = fma(dR[u][i], yh[u][i], s3[i]);
+          }
+          dR[u][i] = mul(dR[u][i], gp[i]);
+          if (p.post_norm == SSTA_NORM_NONE) {
+            if (alive) store8(static_cast<T*>(a.dy) + row_at + i * step, dR[u][i]);
+          } else {
+            q1[u] += sum(dR[u][i]);
+            q2[u] += dot(dR[u][i], yh[u][i]);
           }
         }
-        row_sum2<HALF>(m1, m2, p, exchange[it & 1][1], slot);
-        m1 = p.post_norm == SSTA_NORM_LAYER ? m1 * p.inv_c : 0.f;
-        m2 *= p.inv_c;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) dR[j] = sc.prstd * (dR[j] - m1 - yh[j] * m2);
       }
-      if (alive) store8(static_cast<T*>(a.dy) + row * p.C + ch, dR);
     }
-    prefetch(it + K::kStages);   // into the slot just read
+    if constexpr (POST) {
+      if (p.post_norm != SSTA_NORM_NONE) {
+        row_sums<HALF, U>(q1, q2, warps, exchange[parity][1], slot);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float prstd = table[wr + u].prstd;
+          const float c1 = p.post_norm == SSTA_NORM_LAYER ? -prstd * (q1[u] * p.inv_c) : 0.f;
+          const float c2 = -prstd * (q2[u] * p.inv_c);
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (r0 + u < count && in[i])
+              store8(static_cast<T*>(a.dy) + at0 + (int64_t)(r0 + u) * p.C + i * step,
+                     fma(prstd, dR[u][i], fma(yh[u][i], c2, c1)));
+          }
+        }
+      }
+    }
+    // into the slot just read
+    prefetch(r0 + K::kStages * per_iter, st);
+    st = st + 1 == K::kStages ? 0 : st + 1;
+    parity ^= 1;
   }
 
   if (p.need == 0) return;
   cp_wait<0>();
-  if (p.slots > 1) {
-    // slot 0 adds the other slots' sums in order; the staging memory is free now
-    __syncthreads();
-    float* f = reinterpret_cast<float*>(stage);
-    const int rt = HALF ? 16 : p.row_threads;
-    auto at = [&](int s, int j) -> float& { return f[(s * kSums * kVec + j) * rt + lane]; };
+  if constexpr (NV == 1) {
+    if (p.slots > 1) {
+      // slot 0 adds the other slots' sums in order; the staging memory is free now
+      __syncthreads();
+      uint64_t* f = reinterpret_cast<uint64_t*>(stage);
+      const int rt = HALF ? 16 : p.row_threads;
+      auto at = [&](int sl, int k, int j) -> uint64_t& { return f[((sl * kSums + k) * 4 + j) * rt + lane]; };
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      at(slot, j) = s1[j];
-      at(slot, kVec + j) = s2[j];
-      at(slot, 2 * kVec + j) = s3[j];
-    }
-    __syncthreads();
-    if (slot > 0) return;
-    for (int o = 1; o < p.slots; ++o) {
+      for (int j = 0; j < 4; ++j) {
+        at(slot, 0, j) = s1[0].p[j];
+        at(slot, 1, j) = s2[0].p[j];
+        if constexpr (POST) at(slot, 2, j) = s3[0].p[j];
+      }
+      __syncthreads();
+      if (slot > 0) return;
+      for (int o = 1; o < p.slots; ++o) {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        s1[j] += at(o, j);
-        s2[j] += at(o, kVec + j);
-        s3[j] += at(o, 2 * kVec + j);
+        for (int j = 0; j < 4; ++j) {
+          s1[0].p[j] = f2_add(s1[0].p[j], at(o, 0, j));
+          s2[0].p[j] = f2_add(s2[0].p[j], at(o, 1, j));
+          if constexpr (POST) s3[0].p[j] = f2_add(s3[0].p[j], at(o, 2, j));
+        }
       }
     }
   }
-  if (!in) return;
-  float* out = p.partial + (int64_t)item * kSums * p.C + ch;
-  if (p.need & kNeedS1) store8(out, s1);
-  if (p.need & kNeedS2) store8(out + p.C, s2);
-  if (p.need & kNeedS3) store8(out + 2 * (int64_t)p.C, s3);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (!in[i]) continue;
+    float* out = p.partial + (int64_t)item * kSums * p.C + lane * kVec + i * step;
+    if (p.need & kNeedS1) store8(out, s1[i]);
+    if (p.need & kNeedS2) store8(out + p.C, s2[i]);
+    if constexpr (POST) {
+      if (p.need & kNeedS3) store8(out + 2 * (int64_t)p.C, s3[i]);
+    }
+  }
 }
 
 // Sums of the runs of each group, in order, and the modulation's gradients from them;
@@ -433,40 +509,44 @@ __global__ void __launch_bounds__(1024) norm_bwd_weights_kernel(const __grid_con
   }
 }
 
-template <typename T, bool CODES, bool POST, bool HALF, int MAXT>
+template <typename T, int SRC, bool POST, bool HALF, int NV, int U, int MAXT>
 cudaError_t launch_rows(const BwdParams& p, unsigned blocks, int threads, cudaStream_t s) {
-  using K = Kernel<T, CODES, POST, HALF, MAXT>;
-  const int smem = K::kSmem / MAXT * threads;
+  using K = Kernel<T, SRC, POST, HALF, NV, U, MAXT>;
   static std::atomic<bool> attr_set[64];
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = norm_bwd_kernel<T, CODES, POST, HALF, MAXT>;
+  auto kernel = norm_bwd_kernel<T, SRC, POST, HALF, NV, U, MAXT>;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  kernel<<<blocks, threads, smem, s>>>(p);
+  kernel<<<blocks, threads, K::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, bool CODES, bool POST>
+template <typename T, int SRC, bool POST>
 cudaError_t launch_shape(const BwdParams& p, unsigned blocks, cudaStream_t s) {
   const int threads = p.row_threads * p.slots;
-  if (p.row_threads == 16) return launch_rows<T, CODES, POST, true, 256>(p, blocks, threads, s);
-  if (threads <= 256) return launch_rows<T, CODES, POST, false, 256>(p, blocks, threads, s);
-  if (threads <= 512) return launch_rows<T, CODES, POST, false, 512>(p, blocks, threads, s);
-  return launch_rows<T, CODES, POST, false, 1024>(p, blocks, threads, s);
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;   // fp32 rows are twice as long in shared memory
+  if (p.row_threads == 16) return launch_rows<T, SRC, POST, true, 1, U, 256>(p, blocks, threads, s);
+  if (p.row_threads * kVec < p.C) return launch_rows<T, SRC, POST, false, 2, 1, 512>(p, blocks, threads, s);
+  if (threads <= 256) return launch_rows<T, SRC, POST, false, 1, U, 256>(p, blocks, threads, s);
+  return launch_rows<T, SRC, POST, false, 1, U, 512>(p, blocks, threads, s);
+}
+
+template <typename T, bool POST>
+cudaError_t launch_source(const BwdParams& p, unsigned blocks, cudaStream_t s) {
+  if (p.a.r_saved.codes == nullptr && p.a.y_saved.codes == nullptr) return launch_shape<T, 0, POST>(p, blocks, s);
+  return p.format == SSTA_INT8 ? launch_shape<T, 1 + SSTA_INT8, POST>(p, blocks, s)
+                               : launch_shape<T, 1 + SSTA_E4M3, POST>(p, blocks, s);
 }
 
 template <typename T>
 cudaError_t launch_type(const BwdParams& p, unsigned blocks, cudaStream_t s) {
-  const bool codes = p.a.r_saved.codes != nullptr || p.a.y_saved.codes != nullptr;
-  if (p.a.dy != nullptr)
-    return codes ? launch_shape<T, true, true>(p, blocks, s) : launch_shape<T, false, true>(p, blocks, s);
-  return codes ? launch_shape<T, true, false>(p, blocks, s) : launch_shape<T, false, false>(p, blocks, s);
+  return p.a.dy != nullptr ? launch_source<T, true>(p, blocks, s) : launch_source<T, false>(p, blocks, s);
 }
 
 }  // namespace

@@ -4,10 +4,10 @@
 // Every row is read once, held in registers, and written once: the statistics (mean, then
 // the mean square of the differences, both fp32) are sums over registers and warp
 // shuffles, so the kernel moves 2 (norm) or 4 (residual) elements per channel and is
-// bound by HBM.  A row belongs to one warp up to 2,048 channels (half a warp up to 128)
-// and to 2 or 4 warps above, which exchange their partial sums through shared memory;
-// up to 8 vectors of 8 channels per lane and array keep enough loads in flight without
-// any staging.  Weights and modulation rows are shared by many rows and come from L1/L2.
+// bound by HBM.  A row belongs to one warp up to 1,024 channels (half a warp up to 128)
+// and to 2, 4 or 8 warps above, which exchange their partial sums through shared memory;
+// a thread holds four vectors of 8 channels per array, of one wide row or of several
+// narrow ones, which keeps enough loads in flight without any staging.  Weights and modulation rows are shared by many rows and come from L1/L2.
 // An 8-bit checkpoint of an input or of r is written in the same pass from the registers.
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
@@ -29,181 +29,209 @@ struct FwdParams {
   float eps, res_scale, inv_c;
 };
 
-// Sum of v over the lanes (and warps) of a row; every thread of the row gets it.
-template <int LPR, int WPR>
-__device__ __forceinline__ float row_sum(float v, float* exchange, int slot) {
+// Sums of v[u] over the lanes (and warps) of U rows; every thread of a row gets its row's.
+// `exchange` is used by one call only: a second sum never meets readers of the first.
+template <int U, int LPR, int WPR>
+__device__ __forceinline__ void row_sums(float (&v)[U], float (*exchange)[kFwdThreads / 32], int slot) {
 #pragma unroll
-  for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  for (int off = LPR / 2; off > 0; off >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], off);
   if constexpr (WPR > 1) {
     const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) exchange[warp] = v;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) exchange[u][warp] = v[u];
+    }
     asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(WPR * 32) : "memory");
-    v = 0.f;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) v += exchange[slot * WPR + w];
+    for (int u = 0; u < U; ++u) {
+      v[u] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) v[u] += exchange[u][slot * WPR + w];
+    }
   }
-  return v;
 }
 
-// mean and 1 / deviation of the row in v (lanes beyond C hold zeros in v and are left out).
-template <int NV, int LPR, int WPR>
-__device__ __forceinline__ void row_stats(const float (&v)[NV][kVec], const FwdParams& p, int kind, int lane,
-                                          float* exchange, int slot, float& mean, float& rstd) {
-  mean = 0.f;
+// mean and 1 / deviation of U rows (channels beyond C hold zeros in v and are left out).
+template <int NV, int U, int LPR, int WPR>
+__device__ __forceinline__ void row_stats(const V8 (&v)[U][NV], const FwdParams& p, int kind, int lane,
+                                          float (*exchange)[kFwdThreads / 32], int slot, float (&mean)[U],
+                                          float (&rstd)[U]) {
+  float t[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) mean[u] = 0.f;
   if (kind == SSTA_NORM_LAYER) {
-    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int u = 0; u < U; ++u) {
+      V8 s = v[u][0];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) s += v[i][j];
-    mean = row_sum<LPR, WPR>(s, exchange, slot) * p.inv_c;
-  }
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if ((i * LPR * WPR + lane) * kVec < p.C) {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float d = v[i][j] - mean;
-        q = fmaf(d, d, q);
-      }
+      for (int i = 1; i < NV; ++i) s = add(s, v[u][i]);
+      t[u] = sum(s);
     }
+    row_sums<U, LPR, WPR>(t, exchange, slot);
+#pragma unroll
+    for (int u = 0; u < U; ++u) mean[u] = t[u] * p.inv_c;
   }
-  // exchange + 8: the second sum of a row never meets readers of the first
-  rstd = rsqrtf(row_sum<LPR, WPR>(q, exchange + kFwdThreads / 32, slot) * p.inv_c + p.eps);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    V8 q = fill(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const V8 d = add(v[u][i], fill((i * LPR * WPR + lane) * kVec < p.C ? -mean[u] : 0.f));
+      q = fma(d, d, q);
+    }
+    t[u] = sum(q);
+  }
+  row_sums<U, LPR, WPR>(t, exchange + U, slot);
+#pragma unroll
+  for (int u = 0; u < U; ++u) rstd[u] = rsqrtf(t[u] * p.inv_c + p.eps);
 }
 
-template <int NV, int LPR, int WPR>
-__device__ __forceinline__ void save_row(const float (&v)[NV][kVec], const FwdParams& p, const ssta_checkpoint& c,
-                                         uint32_t row, int lane, bool alive) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int ch = (i * LPR * WPR + lane) * kVec;
-    const int E = group_exponent(group_amax(v[i]), c.format);
-    if (alive && ch < p.C) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.codes) + (int64_t)row * p.C + ch) = encode8(v[i], E, c.format);
-      if (ch % kGroup == 0) c.exponents[(int64_t)row * p.groups_per_row + ch / kGroup] = (uint8_t)E;
-    }
+__device__ __forceinline__ void save8(const V8& v, const FwdParams& p, const ssta_checkpoint& c, uint32_t row, int ch,
+                                      bool in) {
+  const int E = group_exponent(group_amax(v), c.format);
+  if (in) {
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(c.codes) + (int64_t)row * p.C + ch) = encode8(v, E, c.format);
+    if (ch % kGroup == 0) c.exponents[(int64_t)row * p.groups_per_row + ch / kGroup] = (uint8_t)E;
   }
 }
 
-// NV vectors per lane, LPR lanes and WPR warps per row; POST: with a gated residual.
-template <typename T, typename P, int NV, int LPR, int WPR, bool POST>
-__global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(const __grid_constant__ FwdParams p) {
+template <typename P>
+__device__ __forceinline__ V8 param8(const void* v, int64_t at, bool in) {
+  return in ? load8(static_cast<const P*>(v) + at) : fill(0.f);
+}
+
+// NV vectors per lane and row, U rows per thread, LPR lanes and WPR warps per row; POST:
+// with a gated residual.
+template <typename T, typename P, int NV, int U, int LPR, int WPR, bool POST>
+__global__ void __launch_bounds__(kFwdThreads, !POST ? 3 : sizeof(T) == 2 && WPR > 1 ? 3 : 2) norm_fwd_kernel(const __grid_constant__ FwdParams p) {
   constexpr int kRowThreads = LPR * WPR, kSlots = kFwdThreads / kRowThreads;
-  __shared__ float exchange[4][kFwdThreads / 32];
+  __shared__ float exchange[4 * U][kFwdThreads / 32];
   const int slot = threadIdx.x / kRowThreads, lane = threadIdx.x % kRowThreads;
-  const uint32_t row = blockIdx.x * kSlots + slot;
-  const bool alive = row < p.rows;   // dead rows go along with the shuffles and barriers
+  const uint32_t row0 = (blockIdx.x * kSlots + slot) * U;   // rows past the end go along with shuffles and barriers
   const NormFwdArgs& a = p.a;
-  const int64_t base = (int64_t)row * p.C;
+  const int64_t base = (int64_t)row0 * p.C;
   const T* x = static_cast<const T*>(a.x) + base;
   const T* y = static_cast<const T*>(a.y) + base;
-  Raw<T> xr[NV], yr[POST ? NV : 1];
+  Raw<T> xr[U][NV], yr[POST ? U : 1][POST ? NV : 1];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int ch = (i * kRowThreads + lane) * kVec;
-    const bool in = alive && ch < p.C;
-    xr[i] = in ? load_raw(x + ch) : zero_raw<T>();
-    if constexpr (POST) yr[i] = in ? load_raw(y + ch) : zero_raw<T>();
-  }
-  const int64_t mod = p.mod_rows < p.rows ? (int64_t)(row / p.mod_rows) * p.mod_stride : 0;
-  float v[NV][kVec];
-  if constexpr (POST) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) unpack(yr[i], v[i]);
-    if (a.y_save.codes != nullptr) save_row<NV, LPR, WPR>(v, p, a.y_save, row, lane, alive);
-    float pm = 0.f, pr = 1.f;
-    if (p.post_norm != SSTA_NORM_NONE) {
-      row_stats<NV, LPR, WPR>(v, p, p.post_norm, lane, exchange[0], slot, pm, pr);
-      if (alive && lane == 0) {
-        if (a.post_mean != nullptr) a.post_mean[row] = pm;
-        if (a.post_rstd != nullptr) a.post_rstd[row] = pr;
-      }
-    }
+  for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int ch = (i * kRowThreads + lane) * kVec;
-      if (!(alive && ch < p.C)) continue;   // stays zero
-      if (p.post_norm != SSTA_NORM_NONE) {
+      const bool in = row0 + u < p.rows && ch < p.C;
+      xr[u][i] = in ? load_raw(x + u * p.C + ch) : zero_raw<T>();
+      if constexpr (POST) yr[u][i] = in ? load_raw(y + u * p.C + ch) : zero_raw<T>();
+    }
+  }
+  // rows of a thread may belong to different modulation rows
+  int64_t mod[U];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[i][j] = (v[i][j] - pm) * pr;
-        if (a.post_weight != nullptr) {
-          float w[kVec];
-          load8(static_cast<const P*>(a.post_weight) + ch, w);
+  for (int u = 0; u < U; ++u) mod[u] = p.mod_rows < p.rows ? (int64_t)((row0 + u) / p.mod_rows) * p.mod_stride : 0;
+  V8 v[U][NV];
+  float mean[U], rstd[U];
+  if constexpr (POST) {
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) v[i][j] *= w[j];
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[u][i] = unpack(yr[u][i]);
+    if (a.y_save.codes != nullptr) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int ch = (i * kRowThreads + lane) * kVec;
+          save8(v[u][i], p, a.y_save, row0 + u, ch, row0 + u < p.rows && ch < p.C);
+        }
+    }
+    if (p.post_norm != SSTA_NORM_NONE) {
+      row_stats<NV, U, LPR, WPR>(v, p, p.post_norm, lane, exchange, slot, mean, rstd);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (row0 + u < p.rows && lane == 0) {
+          if (a.post_mean != nullptr) a.post_mean[row0 + u] = mean[u];
+          if (a.post_rstd != nullptr) a.post_rstd[row0 + u] = rstd[u];
         }
       }
-      if (a.gate != nullptr) {
-        float w[kVec];
-        load8(static_cast<const P*>(a.gate) + mod + ch, w);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[i][j] = __fmul_rn(v[i][j], w[j]);
+      for (int i = 0; i < NV; ++i) {
+        const int ch = (i * kRowThreads + lane) * kVec;
+        const V8 w = a.post_weight != nullptr ? param8<P>(a.post_weight, ch, ch < p.C) : fill(1.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u][i] = mul(mul(add(v[u][i], fill(-mean[u])), rstd[u]), w);
       }
-      // products and sum rounded one by one: r does not depend on what the compiler fuses
-      float xv[kVec];
-      unpack(xr[i], xv);
+    }
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] = __fadd_rn(__fmul_rn(p.res_scale, xv[j]), v[i][j]);
-      const Raw<T> out = pack(v[i], T());
-      store_raw(static_cast<T*>(a.r) + base + ch, out);
-      xr[i] = out;   // r as stored, for its checkpoint
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int ch = (i * kRowThreads + lane) * kVec;
+        const bool in = row0 + u < p.rows && ch < p.C;
+        if (a.gate != nullptr) v[u][i] = mul(v[u][i], param8<P>(a.gate, mod[u] + ch, in));
+        // products and sum rounded one by one: r does not depend on what gets fused
+        v[u][i] = add(mul(unpack(xr[u][i]), p.res_scale), v[u][i]);
+        if (!in) v[u][i] = fill(0.f);
+        xr[u][i] = pack(v[u][i], T());   // r as stored
+        if (in) store_raw(static_cast<T*>(a.r) + base + u * p.C + ch, xr[u][i]);
+      }
     }
     if (a.r_save.codes != nullptr) {
-      float s[NV][kVec];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) unpack(xr[i], s[i]);
-      save_row<NV, LPR, WPR>(s, p, a.r_save, row, lane, alive);
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int ch = (i * kRowThreads + lane) * kVec;
+          save8(unpack(xr[u][i]), p, a.r_save, row0 + u, ch, row0 + u < p.rows && ch < p.C);
+        }
     }
+    if (p.norm == SSTA_NORM_NONE) return;
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) unpack(xr[i], v[i]);
-    if (a.r_save.codes != nullptr) save_row<NV, LPR, WPR>(v, p, a.r_save, row, lane, alive);
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int ch = (i * kRowThreads + lane) * kVec;
+        v[u][i] = unpack(xr[u][i]);
+        if (a.r_save.codes != nullptr) save8(v[u][i], p, a.r_save, row0 + u, ch, row0 + u < p.rows && ch < p.C);
+      }
+    }
   }
-  if (p.norm == SSTA_NORM_NONE) return;
-  float mean, rstd;
-  row_stats<NV, LPR, WPR>(v, p, p.norm, lane, exchange[2], slot, mean, rstd);
-  if (alive && lane == 0) {
-    if (a.mean != nullptr) a.mean[row] = mean;
-    if (a.rstd != nullptr) a.rstd[row] = rstd;
+  row_stats<NV, U, LPR, WPR>(v, p, p.norm, lane, exchange + 2 * U, slot, mean, rstd);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (row0 + u < p.rows && lane == 0) {
+      if (a.mean != nullptr) a.mean[row0 + u] = mean[u];
+      if (a.rstd != nullptr) a.rstd[row0 + u] = rstd[u];
+    }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int ch = (i * kRowThreads + lane) * kVec;
-    if (!(alive && ch < p.C)) continue;
+    const V8 w = a.weight != nullptr ? param8<P>(a.weight, ch, ch < p.C) : fill(1.f);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) v[i][j] = (v[i][j] - mean) * rstd;
-    if (a.weight != nullptr) {
-      float w[kVec];
-      load8(static_cast<const P*>(a.weight) + ch, w);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] *= w[j];
+    for (int u = 0; u < U; ++u) {
+      const bool in = row0 + u < p.rows && ch < p.C;
+      V8 n = mul(add(v[u][i], fill(-mean[u])), rstd[u]);
+      if (a.weight != nullptr) n = mul(n, w);
+      if (a.scale != nullptr) n = fma(n, param8<P>(a.scale, mod[u] + ch, in), n);
+      if (a.shift != nullptr) n = add(n, param8<P>(a.shift, mod[u] + ch, in));
+      if (in) store8(static_cast<T*>(a.n) + base + u * p.C + ch, n);
     }
-    if (a.scale != nullptr) {
-      float w[kVec];
-      load8(static_cast<const P*>(a.scale) + mod + ch, w);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] = fmaf(v[i][j], w[j], v[i][j]);
-    }
-    if (a.shift != nullptr) {
-      float w[kVec];
-      load8(static_cast<const P*>(a.shift) + mod + ch, w);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] += w[j];
-    }
-    store8(static_cast<T*>(a.n) + base + ch, v[i]);
   }
 }
 
 template <typename T, typename P, int NV, int LPR, int WPR>
 cudaError_t launch_shape(const FwdParams& p, cudaStream_t s) {
-  constexpr int kSlots = kFwdThreads / (LPR * WPR);
-  const unsigned blocks = (p.rows + kSlots - 1) / kSlots;
-  if (p.a.y != nullptr)
-    norm_fwd_kernel<T, P, NV, LPR, WPR, true><<<blocks, kFwdThreads, 0, s>>>(p);
-  else
-    norm_fwd_kernel<T, P, NV, LPR, WPR, false><<<blocks, kFwdThreads, 0, s>>>(p);
+  // four vectors per thread and array; half the rows where two arrays are held
+  constexpr int kU = 4 / NV, kUPost = kU > 1 ? kU / 2 : 1, kSlots = kFwdThreads / (LPR * WPR);
+  if (p.a.y != nullptr) {
+    const unsigned blocks = (p.rows + kSlots * kUPost - 1) / (kSlots * kUPost);
+    norm_fwd_kernel<T, P, NV, kUPost, LPR, WPR, true><<<blocks, kFwdThreads, 0, s>>>(p);
+  } else {
+    const unsigned blocks = (p.rows + kSlots * kU - 1) / (kSlots * kU);
+    norm_fwd_kernel<T, P, NV, kU, LPR, WPR, false><<<blocks, kFwdThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 
@@ -213,9 +241,9 @@ cudaError_t launch_types(const FwdParams& p, cudaStream_t s) {
   if (p.C <= 256) return launch_shape<T, P, 1, 32, 1>(p, s);
   if (p.C <= 512) return launch_shape<T, P, 2, 32, 1>(p, s);
   if (p.C <= 1024) return launch_shape<T, P, 4, 32, 1>(p, s);
-  if (p.C <= 2048) return launch_shape<T, P, 8, 32, 1>(p, s);
-  if (p.C <= 4096) return launch_shape<T, P, 8, 32, 2>(p, s);
-  return launch_shape<T, P, 8, 32, 4>(p, s);
+  if (p.C <= 2048) return launch_shape<T, P, 4, 32, 2>(p, s);
+  if (p.C <= 4096) return launch_shape<T, P, 4, 32, 4>(p, s);
+  return launch_shape<T, P, 4, 32, 8>(p, s);
 }
 
 }  // namespace
