@@ -38,6 +38,9 @@ constexpr int kNeedS1 = 1, kNeedS2 = 2, kNeedS3 = 4;
 
 struct BwdParams {
   NormBwdArgs a;
+  // what is copied row by row; an absent tensor has some valid address and reads as zeros
+  const void *dn, *dr, *r, *y;
+  bool has_n, has_r, has_y;
   float* partial;   // [groups * chunks][kSums][C]
   uint32_t rows, mod_rows, chunk_rows;
   int64_t mod_stride;
@@ -94,16 +97,30 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool li
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A thread's slot for one vector of a dense tensor: 16-byte planes, one entry per thread
-// in each (neighbouring threads' 16 bytes are neighbours, no bank conflicts).
-template <int MAXT>
-__device__ __forceinline__ void copy_dense(uint32_t slot, const __nv_bfloat16* src, bool live) {
-  cp_async16(slot + threadIdx.x * 16, src, live);
+// One vector of a dense tensor per thread of the block in shared memory.  bf16: the
+// thread's own 16 bytes.  fp32: 16-byte halves in two planes, copied so that neighbouring
+// lanes read neighbouring 16 bytes (a thread reading its own 32 would fetch every sector
+// twice), that is partly for other lanes of its LANES: warps synchronise around it.  The
+// second plane is shifted by half the banks, so neither side has conflicts.
+template <typename T, int MAXT> constexpr int kDenseBytes = (int)sizeof(T) * kVec * MAXT + (sizeof(T) == 4 ? 64 : 0);
+
+// `off` is the offset of channel `ch`, the thread's first, from src; src itself is always
+// valid to address.
+template <int MAXT, int LANES>
+__device__ __forceinline__ void copy_dense(uint32_t slot, const __nv_bfloat16* src, uint32_t off, int ch, int C, bool live) {
+  const bool ok = live && ch < C;
+  cp_async16(slot + threadIdx.x * 16, src + (ok ? off : 0), ok);
 }
-template <int MAXT>
-__device__ __forceinline__ void copy_dense(uint32_t slot, const float* src, bool live) {
-  cp_async16(slot + threadIdx.x * 16, src, live);
-  cp_async16(slot + (MAXT + threadIdx.x) * 16, src + 4, live);
+template <int MAXT, int LANES>
+__device__ __forceinline__ void copy_dense(uint32_t slot, const float* src, uint32_t off, int ch, int C, bool live) {
+  const int l = threadIdx.x % LANES;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = l + j * LANES;                 // 16-byte chunk among those of LANES vectors
+    const int d = c * 4 - l * kVec;              // from this thread's own first channel
+    const bool ok = live && ch + d < C;
+    cp_async16(slot + (c & 1) * (MAXT * 16 + 64) + (threadIdx.x - l + (c >> 1)) * 16, src + (ok ? off + d : 0), ok);
+  }
 }
 template <int MAXT>
 __device__ __forceinline__ V8 read_dense(const uint8_t* slot, __nv_bfloat16) {
@@ -112,7 +129,7 @@ __device__ __forceinline__ V8 read_dense(const uint8_t* slot, __nv_bfloat16) {
 template <int MAXT>
 __device__ __forceinline__ V8 read_dense(const uint8_t* slot, float) {
   return unpack(Raw<float>{reinterpret_cast<const float4*>(slot)[threadIdx.x],
-                           reinterpret_cast<const float4*>(slot)[MAXT + threadIdx.x]});
+                           reinterpret_cast<const float4*>(slot + MAXT * 16 + 64)[threadIdx.x]});
 }
 
 // Sums of a[u] and b[u] over the threads of each of U rows (1 or 2); every thread of the
@@ -160,21 +177,25 @@ __device__ __forceinline__ void row_sums(float (&a)[U], float (&b)[U], int warps
 }
 
 // What a row brings besides its channels, in shared memory for kWindow rows at a time:
-// xh = v * scale + shift of both norms, and the checkpoints' exponent bytes.
+// xh = v * scale + shift of both norms, with one scale per checkpoint group (the code's
+// scale times 1 / deviation) where r and y are codes.
 constexpr int kWindow = 64;   // a multiple of the rows a block takes at once (at most 32)
 struct RowScalars {
   float rstd, shift, prstd, pshift;
 };
 
+// What stands behind the norm's gradient: nothing, a gate, a gate and a post norm.
+enum Post { kNoPost = 0, kGate = 1, kPostNorm = 2 };
+
 // SRC: 0 dense r and y, 1 + format: checkpoints.
-template <typename T, int SRC, bool POST, bool HALF, int NV, int U, int MAXT>
+template <typename T, int SRC, int POST, bool HALF, int NV, int U, int MAXT>
 struct Kernel {
-  // bytes of a thread's slots per vector: dn, dr, r and (behind a gated residual) y
-  static constexpr int kDense = (int)sizeof(T) * kVec, kKept = SRC ? 8 : kDense;
-  static constexpr int kVecBytes = 2 * kDense + (POST ? 2 : 1) * kKept;
-  static constexpr int kStageBytes = NV * U * kVecBytes * MAXT;
-  static constexpr int kExps = SRC ? MAXT * NV * kVec / kGroup : 0;   // exponent bytes of a row
-  static constexpr int kTable = kWindow * ((int)sizeof(RowScalars) + (POST ? 2 : 1) * kExps);
+  static constexpr int kKept = SRC ? 8 * MAXT : kDenseBytes<T, MAXT>;   // r, y
+  // places of a vector's dn, dr, r and y
+  static constexpr int kR = 2 * kDenseBytes<T, MAXT>, kY = kR + kKept, kVecBytes = POST ? kY + kKept : kY;
+  static constexpr int kStageBytes = NV * U * kVecBytes;
+  static constexpr int kScales = SRC ? MAXT * NV * kVec / kGroup : 0;   // group scales of a row
+  static constexpr int kTable = kWindow * ((int)sizeof(RowScalars) + (POST ? 2 : 1) * kScales * 4);
   // copies in flight: up to four times U rows, as far as shared memory goes (two blocks of
   // 256 threads, or one larger one, per SM)
   static constexpr int kFit = ((MAXT <= 256 ? 112 : 224) * 1024 - kTable) / kStageBytes;
@@ -183,15 +204,15 @@ struct Kernel {
   static constexpr int kSmem = kTable + (kStages * kStageBytes > kSumBytes ? kStages * kStageBytes : kSumBytes);
 };
 
-template <typename T, int SRC, bool POST, bool HALF, int NV, int U, int MAXT>
+template <typename T, int SRC, int POST, bool HALF, int NV, int U, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ BwdParams p) {
   using K = Kernel<T, SRC, POST, HALF, NV, U, MAXT>;
-  constexpr int kFormat = SRC - 1;
+  constexpr int kLanes = HALF ? 16 : 32;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float exchange[2][2][2 * U * (MAXT / 32)];
   RowScalars* const table = reinterpret_cast<RowScalars*>(smem);
-  uint8_t* const exps_r = smem + kWindow * sizeof(RowScalars);
-  uint8_t* const exps_y = exps_r + kWindow * K::kExps;
+  float* const scales_r = reinterpret_cast<float*>(smem + kWindow * sizeof(RowScalars));
+  float* const scales_y = scales_r + kWindow * K::kScales;
   uint8_t* const stage = smem + K::kTable;
   const NormBwdArgs& a = p.a;
   const int warps = p.row_threads >> 5;
@@ -204,76 +225,71 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   const int64_t group_end = min(group_first + p.mod_rows, (int64_t)p.rows);
   const int count = (int)max(min((int64_t)p.chunk_rows, group_end - first), (int64_t)0);   // rows of this run
   const int per_iter = p.slots * U;
-  const bool has_n = a.dn != nullptr, has_r = a.dr != nullptr;
-  const bool has_y = POST && (a.y != nullptr || a.y_saved.codes != nullptr);
   bool in[NV];   // this vector's channels exist
 #pragma unroll
   for (int i = 0; i < NV; ++i) in[i] = lane * kVec + i * step < p.C;
+  // an element is addressed by the block's row (the same for all threads) and this offset
+  const uint32_t mine = slot * U * p.C + lane * kVec;
 
   const uint32_t stage0 = (uint32_t)__cvta_generic_to_shared(stage);
-  const int64_t at0 = first * p.C + lane * kVec;   // this thread's first channel in row `first`
-  auto prefetch = [&](int r0, int st) {   // rows r0 .. of this thread's slot into stage st
-    const uint32_t base = stage0 + st * K::kStageBytes;
+  auto prefetch = [&](int done, int st) {   // rows done + slot * U .. into stage st
+    const int64_t at = min(first + min(done, max(count - 1, 0)), (int64_t)p.rows - 1) * p.C;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t row_at = r0 + u < count ? at0 + (int64_t)(r0 + u) * p.C : at0;
+      const bool live = done + slot * U + u < count;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const bool live = r0 + u < count && in[i];
-        const int64_t at = live ? row_at + i * step : 0;
-        const uint32_t s = base + (u * NV + i) * (K::kVecBytes * MAXT);
-        if (has_n) {
-          copy_dense<MAXT>(s, static_cast<const T*>(a.dn) + at, live);
-          if constexpr (SRC) cp_async8(s + 2 * K::kDense * MAXT + threadIdx.x * 8, static_cast<const uint8_t*>(a.r_saved.codes) + at, live);
-          else copy_dense<MAXT>(s + 2 * K::kDense * MAXT, static_cast<const T*>(a.r) + at, live);
-        }
-        if (has_r) copy_dense<MAXT>(s + K::kDense * MAXT, static_cast<const T*>(a.dr) + at, live);
-        if constexpr (POST) {
-          constexpr int kY = (2 * K::kDense + K::kKept) * MAXT;
-          if (has_y) {
-            if constexpr (SRC) cp_async8(s + kY + threadIdx.x * 8, static_cast<const uint8_t*>(a.y_saved.codes) + at, live);
-            else copy_dense<MAXT>(s + kY, static_cast<const T*>(a.y) + at, live);
+        const int ch = lane * kVec + i * step;
+        const uint32_t off = mine + u * p.C + i * step, s = stage0 + st * K::kStageBytes + (u * NV + i) * K::kVecBytes;
+        auto copy_kept = [&](uint32_t to, const void* src, bool has) {
+          if constexpr (SRC) {
+            const bool ok = live && has && in[i];
+            cp_async8(to + threadIdx.x * 8, static_cast<const uint8_t*>(src) + at + (ok ? off : 0), ok);
+          } else {
+            copy_dense<MAXT, kLanes>(to, static_cast<const T*>(src) + at, off, ch, p.C, live && has);
           }
-        }
+        };
+        copy_dense<MAXT, kLanes>(s, static_cast<const T*>(p.dn) + at, off, ch, p.C, live && p.has_n);
+        copy_dense<MAXT, kLanes>(s + kDenseBytes<T, MAXT>, static_cast<const T*>(p.dr) + at, off, ch, p.C, live && p.has_r);
+        copy_kept(s + K::kR, p.r, p.has_n);
+        if constexpr (POST) copy_kept(s + K::kY, p.y, p.has_y);
       }
     }
     cp_commit();
   };
-  // Fills the table for the kWindow rows from w0 on (a row that does not exist has rstd 0
-  // and readable exponents).
+  // Fills the table for the kWindow rows from w0 on (rstd 0 where there is no row).
   auto fill_table = [&](int w0) {
     __syncthreads();
     for (int r = threadIdx.x; r < kWindow; r += blockDim.x) {
-      RowScalars v{0.f, 0.f, 1.f, 0.f};
+      RowScalars v{0.f, 0.f, POST == kPostNorm ? 0.f : 1.f, 0.f};
       if (w0 + r < count) {
         const int64_t row = first + w0 + r;
-        if (has_n) {
+        if (p.has_n) {
           v.rstd = a.rstd[row];
           if (p.norm == SSTA_NORM_LAYER) v.shift = -a.mean[row] * v.rstd;
         }
-        if constexpr (POST) {
-          if (p.post_norm != SSTA_NORM_NONE) v.prstd = a.post_rstd[row];
+        if constexpr (POST == kPostNorm) {
+          v.prstd = a.post_rstd[row];
           if (p.post_norm == SSTA_NORM_LAYER) v.pshift = -a.post_mean[row] * v.prstd;
         }
       }
       table[r] = v;
     }
     if constexpr (SRC) {
+      __syncthreads();
       const int64_t from = (first + w0) * p.groups_per_row;
       const int n = min(kWindow, count - w0) * p.groups_per_row;
       for (int e = threadIdx.x; e < kWindow * p.groups_per_row; e += blockDim.x) {
-        if (has_n) exps_r[e] = e < n ? a.r_saved.exponents[from + e] : 1;
-        if constexpr (POST) {
-          if (has_y) exps_y[e] = e < n ? a.y_saved.exponents[from + e] : 1;
-        }
+        const RowScalars& v = table[e / p.groups_per_row];
+        scales_r[e] = e < n && p.has_n ? code_scale(a.r_saved.exponents[from + e]) * v.rstd : 0.f;
+        if constexpr (POST) scales_y[e] = e < n && p.has_y ? code_scale(a.y_saved.exponents[from + e]) * v.prstd : 0.f;
       }
     }
     __syncthreads();
   };
 
-  int r0 = slot * U;
 #pragma unroll
-  for (int i = 0; i < K::kStages; ++i) prefetch(r0 + i * per_iter, i);
+  for (int i = 0; i < K::kStages; ++i) prefetch(i * per_iter, i);
 
   // products of the vectors for this thread's channels (0 beyond C)
   V8 gw[NV], gp[POST ? NV : 1];
@@ -299,64 +315,63 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   }
 
   int st = 0, parity = 0;
-  for (int done = 0; done < count; done += per_iter, r0 += per_iter) {
+  for (int done = 0; done < count; done += per_iter) {
     if (done % kWindow == 0) fill_table(done);
     cp_wait<K::kStages - 1>();
+    if constexpr (sizeof(T) == 4) __syncwarp();
     const uint8_t* const s = stage + st * K::kStageBytes;
-    const int wr = r0 % kWindow;
-    auto place = [&](int u, int i, int offset) { return s + ((u * NV + i) * K::kVecBytes + offset) * MAXT; };
-    auto kept = [&](int u, int i, int offset, const uint8_t* exps, float scale, float shift) {
+    const int wr = done % kWindow + slot * U;
+    auto place = [&](int u, int i, int offset) { return s + (u * NV + i) * K::kVecBytes + offset; };
+    // (value of r or y) * scale + shift, with the row's scale or the code group's
+    auto kept = [&](int u, int i, int offset, const float* scales, float scale, float shift) {
       if constexpr (SRC) {
-        const int E = exps[(wr + u) * p.groups_per_row + (in[i] ? (lane * kVec + i * step) / kGroup : 0)];
-        return fma(decode8(reinterpret_cast<const uint2*>(place(u, i, offset))[threadIdx.x], kFormat),
-                   code_scale(E) * scale, shift);
+        scale = scales[(wr + u) * p.groups_per_row + (in[i] ? (lane * kVec + i * step) / kGroup : 0)];
+        return fma(decode8(reinterpret_cast<const uint2*>(place(u, i, offset))[threadIdx.x], SRC - 1), scale, shift);
       } else {
         return fma(read_dense<MAXT>(place(u, i, offset), T()), scale, shift);
       }
     };
     V8 g[U][NV], rh[U][NV];
     float m1[U], m2[U];
-    if (has_n) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float2 rs = *reinterpret_cast<const float2*>(&table[wr + u].rstd);
-        m1[u] = m2[u] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      const float2 rs = *reinterpret_cast<const float2*>(&table[wr + u].rstd);
+      m1[u] = m2[u] = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const V8 dn = read_dense<MAXT>(place(u, i, 0), T());
-          rh[u][i] = kept(u, i, 2 * K::kDense, exps_r, rs.x, rs.y);
-          s1[i] = add(s1[i], dn);
-          s2[i] = fma(dn, rh[u][i], s2[i]);
-          g[u][i] = mul(dn, gw[i]);
-          m1[u] += sum(g[u][i]);
-          m2[u] += dot(g[u][i], rh[u][i]);
-        }
+      for (int i = 0; i < NV; ++i) {
+        const V8 dn = read_dense<MAXT>(place(u, i, 0), T());
+        rh[u][i] = kept(u, i, K::kR, scales_r, rs.x, rs.y);
+        s1[i] = add(s1[i], dn);
+        s2[i] = fma(dn, rh[u][i], s2[i]);
+        g[u][i] = mul(dn, gw[i]);
+        m1[u] += sum(g[u][i]);
+        m2[u] += dot(g[u][i], rh[u][i]);
       }
-      row_sums<HALF, U>(m1, m2, warps, exchange[parity][0], slot);
     }
+    row_sums<HALF, U>(m1, m2, warps, exchange[parity][0], slot);
+    T* const dx = static_cast<T*>(a.dx) + (first + done) * p.C;
+    T* const dy = static_cast<T*>(a.dy) + (first + done) * p.C;
     V8 dR[U][NV], yh[POST ? U : 1][POST ? NV : 1];
     float q1[U], q2[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       q1[u] = q2[u] = 0.f;
       const RowScalars sc = table[wr + u];
-      const float c1 = has_n && p.norm == SSTA_NORM_LAYER ? -sc.rstd * (m1[u] * p.inv_c) : 0.f;
-      const float c2 = has_n ? -sc.rstd * (m2[u] * p.inv_c) : 0.f;
-      const int64_t row_at = at0 + (int64_t)(r0 + u) * p.C;
+      const float c1 = p.norm == SSTA_NORM_LAYER ? -sc.rstd * (m1[u] * p.inv_c) : 0.f;
+      const float c2 = -sc.rstd * (m2[u] * p.inv_c);
+      const bool live = done + slot * U + u < count;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        dR[u][i] = has_r ? read_dense<MAXT>(place(u, i, K::kDense), T()) : fill(0.f);
-        if (has_n) dR[u][i] = add(dR[u][i], fma(sc.rstd, g[u][i], fma(rh[u][i], c2, c1)));
-        const bool alive = r0 + u < count && in[i];
-        if (alive) store8(static_cast<T*>(a.dx) + row_at + i * step, POST ? mul(dR[u][i], p.res_scale) : dR[u][i]);
+        const uint32_t off = mine + u * p.C + i * step;
+        dR[u][i] = add(read_dense<MAXT>(place(u, i, kDenseBytes<T, MAXT>), T()),
+                       fma(sc.rstd, g[u][i], fma(rh[u][i], c2, c1)));
+        if (live && in[i]) store8(dx + off, POST ? mul(dR[u][i], p.res_scale) : dR[u][i]);
         if constexpr (POST) {
-          if (has_y) {
-            yh[u][i] = kept(u, i, 2 * K::kDense + K::kKept, exps_y, sc.prstd, sc.pshift);
-            s3[i] = fma(dR[u][i], yh[u][i], s3[i]);
-          }
+          yh[u][i] = kept(u, i, K::kY, scales_y, sc.prstd, sc.pshift);
+          s3[i] = fma(dR[u][i], yh[u][i], s3[i]);
           dR[u][i] = mul(dR[u][i], gp[i]);
-          if (p.post_norm == SSTA_NORM_NONE) {
-            if (alive) store8(static_cast<T*>(a.dy) + row_at + i * step, dR[u][i]);
+          if constexpr (POST == kGate) {
+            if (live && in[i]) store8(dy + off, dR[u][i]);
           } else {
             q1[u] += sum(dR[u][i]);
             q2[u] += dot(dR[u][i], yh[u][i]);
@@ -364,25 +379,23 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
         }
       }
     }
-    if constexpr (POST) {
-      if (p.post_norm != SSTA_NORM_NONE) {
-        row_sums<HALF, U>(q1, q2, warps, exchange[parity][1], slot);
+    if constexpr (POST == kPostNorm) {
+      row_sums<HALF, U>(q1, q2, warps, exchange[parity][1], slot);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float prstd = table[wr + u].prstd;
-          const float c1 = p.post_norm == SSTA_NORM_LAYER ? -prstd * (q1[u] * p.inv_c) : 0.f;
-          const float c2 = -prstd * (q2[u] * p.inv_c);
+      for (int u = 0; u < U; ++u) {
+        const float prstd = table[wr + u].prstd;
+        const float c1 = p.post_norm == SSTA_NORM_LAYER ? -prstd * (q1[u] * p.inv_c) : 0.f;
+        const float c2 = -prstd * (q2[u] * p.inv_c);
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            if (r0 + u < count && in[i])
-              store8(static_cast<T*>(a.dy) + at0 + (int64_t)(r0 + u) * p.C + i * step,
-                     fma(prstd, dR[u][i], fma(yh[u][i], c2, c1)));
-          }
+        for (int i = 0; i < NV; ++i) {
+          if (done + slot * U + u < count && in[i])
+            store8(dy + (mine + u * p.C + i * step), fma(prstd, dR[u][i], fma(yh[u][i], c2, c1)));
         }
       }
     }
-    // into the slot just read
-    prefetch(r0 + K::kStages * per_iter, st);
+    // into the slots just read
+    if constexpr (sizeof(T) == 4) __syncwarp();
+    prefetch(done + K::kStages * per_iter, st);
     st = st + 1 == K::kStages ? 0 : st + 1;
     parity ^= 1;
   }
@@ -509,7 +522,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_weights_kernel(const __grid_con
   }
 }
 
-template <typename T, int SRC, bool POST, bool HALF, int NV, int U, int MAXT>
+template <typename T, int SRC, int POST, bool HALF, int NV, int U, int MAXT>
 cudaError_t launch_rows(const BwdParams& p, unsigned blocks, int threads, cudaStream_t s) {
   using K = Kernel<T, SRC, POST, HALF, NV, U, MAXT>;
   static std::atomic<bool> attr_set[64];
@@ -527,7 +540,7 @@ cudaError_t launch_rows(const BwdParams& p, unsigned blocks, int threads, cudaSt
   return cudaGetLastError();
 }
 
-template <typename T, int SRC, bool POST>
+template <typename T, int SRC, int POST>
 cudaError_t launch_shape(const BwdParams& p, unsigned blocks, cudaStream_t s) {
   const int threads = p.row_threads * p.slots;
   constexpr int U = sizeof(T) == 2 ? 2 : 1;   // fp32 rows are twice as long in shared memory
@@ -537,7 +550,7 @@ cudaError_t launch_shape(const BwdParams& p, unsigned blocks, cudaStream_t s) {
   return launch_rows<T, SRC, POST, false, 1, U, 512>(p, blocks, threads, s);
 }
 
-template <typename T, bool POST>
+template <typename T, int POST>
 cudaError_t launch_source(const BwdParams& p, unsigned blocks, cudaStream_t s) {
   if (p.a.r_saved.codes == nullptr && p.a.y_saved.codes == nullptr) return launch_shape<T, 0, POST>(p, blocks, s);
   return p.format == SSTA_INT8 ? launch_shape<T, 1 + SSTA_INT8, POST>(p, blocks, s)
@@ -546,7 +559,8 @@ cudaError_t launch_source(const BwdParams& p, unsigned blocks, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_type(const BwdParams& p, unsigned blocks, cudaStream_t s) {
-  return p.a.dy != nullptr ? launch_source<T, true>(p, blocks, s) : launch_source<T, false>(p, blocks, s);
+  if (p.a.dy == nullptr) return launch_source<T, kNoPost>(p, blocks, s);
+  return p.post_norm == SSTA_NORM_NONE ? launch_source<T, kGate>(p, blocks, s) : launch_source<T, kPostNorm>(p, blocks, s);
 }
 
 }  // namespace
@@ -562,6 +576,13 @@ cudaError_t launch_norm_bwd(const NormGeom& g, const NormBwdArgs& a, void* works
   FinalParams f{};
   BwdParams& p = f.b;
   p.a = a;
+  p.has_n = a.dn != nullptr;
+  p.has_r = a.dr != nullptr;
+  p.has_y = a.y != nullptr || a.y_saved.codes != nullptr;
+  p.dn = p.has_n ? a.dn : a.dx;
+  p.dr = p.has_r ? a.dr : a.dx;
+  p.r = a.r != nullptr ? a.r : a.r_saved.codes != nullptr ? a.r_saved.codes : a.dx;
+  p.y = a.y != nullptr ? a.y : a.y_saved.codes != nullptr ? a.y_saved.codes : a.dx;
   p.partial = static_cast<float*>(workspace);
   p.rows = (uint32_t)g.rows;
   p.mod_rows = (uint32_t)g.mod_rows;
