@@ -43,16 +43,33 @@ template <> struct Raw<float> { float4 a, b; };
 __device__ __forceinline__ Raw<__nv_bfloat16> load_raw(const __nv_bfloat16* p) {
   return {*reinterpret_cast<const uint4*>(p)};
 }
+// fp32: 32 bytes at once where the tensor allows it (it is 16-byte aligned at least, and
+// rows are whole multiples of 32 bytes), since two 16-byte accesses of a warp touch every
+// 32-byte sector twice.
 __device__ __forceinline__ Raw<float> load_raw(const float* p) {
-  return {reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1]};
+  Raw<float> r;
+  if ((reinterpret_cast<uintptr_t>(p) & 16) == 0)
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r.a.x), "=f"(r.a.y), "=f"(r.a.z), "=f"(r.a.w), "=f"(r.b.x), "=f"(r.b.y), "=f"(r.b.z), "=f"(r.b.w)
+                 : "l"(p)
+                 : "memory");
+  else
+    r = {reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1]};
+  return r;
 }
 template <typename T> __device__ __forceinline__ Raw<T> zero_raw() { return Raw<T>{}; }
 __device__ __forceinline__ void store_raw(__nv_bfloat16* p, const Raw<__nv_bfloat16>& r) {
   *reinterpret_cast<uint4*>(p) = r.a;
 }
 __device__ __forceinline__ void store_raw(float* p, const Raw<float>& r) {
-  reinterpret_cast<float4*>(p)[0] = r.a;
-  reinterpret_cast<float4*>(p)[1] = r.b;
+  if ((reinterpret_cast<uintptr_t>(p) & 16) == 0) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(r.a.x), "f"(r.a.y), "f"(r.a.z),
+                 "f"(r.a.w), "f"(r.b.x), "f"(r.b.y), "f"(r.b.z), "f"(r.b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = r.a;
+    reinterpret_cast<float4*>(p)[1] = r.b;
+  }
 }
 
 // Eight channels in fp32, as four pairs: the kernels' arithmetic runs on pairs
