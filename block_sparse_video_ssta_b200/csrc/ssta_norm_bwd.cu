@@ -177,8 +177,7 @@ __device__ __forceinline__ void row_sums(float (&a)[U], float (&b)[U], int warps
 }
 
 // What a row brings besides its channels, in shared memory for kWindow rows at a time:
-// xh = v * scale + shift of both norms, with one scale per checkpoint group (the code's
-// scale times 1 / deviation) where r and y are codes.
+// xh = v * rstd + shift of both norms, and the codes' scales of each group.
 constexpr int kWindow = 64;   // a multiple of the rows a block takes at once (at most 32)
 struct RowScalars {
   float rstd, shift, prstd, pshift;
@@ -257,32 +256,34 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     }
     cp_commit();
   };
-  // Fills the table for the kWindow rows from w0 on (rstd 0 where there is no row).
+  // Fills the table for the kWindow rows from w0 on (rstd and group scales 0 where there is
+  // no row).  The first kWindow threads fetch the rows' scalars, the others the exponents.
+  static_assert(kWindow == 64, "blocks have at least 160 threads");
   auto fill_table = [&](int w0) {
-    __syncthreads();
-    for (int r = threadIdx.x; r < kWindow; r += blockDim.x) {
+    if (w0 > 0) __syncthreads();
+    if (threadIdx.x < kWindow) {
+      const int r = threadIdx.x;
       RowScalars v{0.f, 0.f, POST == kPostNorm ? 0.f : 1.f, 0.f};
       if (w0 + r < count) {
         const int64_t row = first + w0 + r;
-        if (p.has_n) {
-          v.rstd = a.rstd[row];
-          if (p.norm == SSTA_NORM_LAYER) v.shift = -a.mean[row] * v.rstd;
-        }
+        const bool layer = p.norm == SSTA_NORM_LAYER, post_layer = p.post_norm == SSTA_NORM_LAYER;
+        const float rstd = p.has_n ? a.rstd[row] : 0.f, mean = p.has_n && layer ? a.mean[row] : 0.f;
         if constexpr (POST == kPostNorm) {
-          v.prstd = a.post_rstd[row];
-          if (p.post_norm == SSTA_NORM_LAYER) v.pshift = -a.post_mean[row] * v.prstd;
+          const float prstd = a.post_rstd[row], pmean = post_layer ? a.post_mean[row] : 0.f;
+          v.prstd = prstd;
+          v.pshift = -pmean * prstd;
         }
+        v.rstd = rstd;
+        v.shift = -mean * rstd;
       }
       table[r] = v;
-    }
-    if constexpr (SRC) {
-      __syncthreads();
+    } else if constexpr (SRC) {
       const int64_t from = (first + w0) * p.groups_per_row;
       const int n = min(kWindow, count - w0) * p.groups_per_row;
-      for (int e = threadIdx.x; e < kWindow * p.groups_per_row; e += blockDim.x) {
-        const RowScalars& v = table[e / p.groups_per_row];
-        scales_r[e] = e < n && p.has_n ? code_scale(a.r_saved.exponents[from + e]) * v.rstd : 0.f;
-        if constexpr (POST) scales_y[e] = e < n && p.has_y ? code_scale(a.y_saved.exponents[from + e]) * v.prstd : 0.f;
+#pragma unroll 4
+      for (int e = threadIdx.x - kWindow; e < kWindow * p.groups_per_row; e += blockDim.x - kWindow) {
+        scales_r[e] = e < n && p.has_n ? code_scale(a.r_saved.exponents[from + e]) : 0.f;
+        if constexpr (POST) scales_y[e] = e < n && p.has_y ? code_scale(a.y_saved.exponents[from + e]) : 0.f;
       }
     }
     __syncthreads();
@@ -291,21 +292,32 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
 #pragma unroll
   for (int i = 0; i < K::kStages; ++i) prefetch(i * per_iter, i);
 
-  // products of the vectors for this thread's channels (0 beyond C)
+  // products of the vectors for this thread's channels (0 beyond C); all loads are issued
+  // before the first is used
   V8 gw[NV], gp[POST ? NV : 1];
+  auto products = [&](auto type) {
+    using P = decltype(type);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int ch = lane * kVec + i * step;
-    const int64_t mod = (int64_t)grp * p.mod_stride + ch;
-    gw[i] = fill(in[i] ? 1.f : 0.f);
-    if (in[i] && a.weight != nullptr) gw[i] = load_param8(a.weight, ch, p.param_f32);
-    if (in[i] && a.scale != nullptr) gw[i] = mul(gw[i], add(load_param8(a.scale, mod, p.param_f32), fill(1.f)));
-    if constexpr (POST) {
-      gp[i] = fill(in[i] ? 1.f : 0.f);
-      if (in[i] && a.post_weight != nullptr) gp[i] = load_param8(a.post_weight, ch, p.param_f32);
-      if (in[i] && a.gate != nullptr) gp[i] = mul(gp[i], load_param8(a.gate, mod, p.param_f32));
+    for (int i = 0; i < NV; ++i) {
+      const int ch = lane * kVec + i * step;
+      const int64_t mod = (int64_t)grp * p.mod_stride + ch;
+      Raw<P> w[4];
+      const void* const src[4] = {a.weight, a.scale, a.post_weight, a.gate};
+#pragma unroll
+      for (int k = 0; k < (POST ? 4 : 2); ++k) {
+        w[k] = zero_raw<P>();
+        if (in[i] && src[k] != nullptr) w[k] = load_raw(static_cast<const P*>(src[k]) + (k & 1 ? mod : ch));
+      }
+      const float one = in[i] ? 1.f : 0.f;
+      gw[i] = mul(a.weight != nullptr ? unpack(w[0]) : fill(one), add(unpack(w[1]), fill(one)));
+      if constexpr (POST)
+        gp[i] = mul(a.post_weight != nullptr ? unpack(w[2]) : fill(one), a.gate != nullptr ? unpack(w[3]) : fill(one));
     }
-  }
+  };
+  if (p.param_f32)
+    products(float());
+  else
+    products(__nv_bfloat16());
   V8 s1[NV], s2[NV], s3[POST ? NV : 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i) s1[i] = s2[i] = fill(0.f);
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     // (value of r or y) * scale + shift, with the row's scale or the code group's
     auto kept = [&](int u, int i, int offset, const float* scales, float scale, float shift) {
       if constexpr (SRC) {
-        scale = scales[(wr + u) * p.groups_per_row + (in[i] ? (lane * kVec + i * step) / kGroup : 0)];
+        scale *= scales[(wr + u) * p.groups_per_row + (in[i] ? (lane * kVec + i * step) / kGroup : 0)];
         return fma(decode8(reinterpret_cast<const uint2*>(place(u, i, offset))[threadIdx.x], SRC - 1), scale, shift);
       } else {
         return fma(read_dense<MAXT>(place(u, i, offset), T()), scale, shift);
@@ -441,15 +453,18 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
 
 // Sums of the runs of each group, in order, and the modulation's gradients from them;
 // leaves the group's term of dweight and dpost_weight in its first run's place (or, with
-// one group, writes the gradient).  32 channels per block; 8 threads per channel share a
-// group's runs, or take a group each where a group has few runs.
-constexpr int kFinalY = 8;
+// one group, writes the gradient).  32 channels per block; 16 threads per channel share a
+// group's runs, or take a group each where a group has few runs.  Launched as a
+// programmatic dependent of the kernel before: only its launch overlaps that kernel.
+constexpr int kFinalY = 16;
 struct FinalParams {
   BwdParams b;
   uint32_t groups;
   int channel_blocks;
   bool per_group;   // a group per thread row
 };
+
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __global__ void __launch_bounds__(32 * kFinalY) norm_bwd_groups_kernel(const __grid_constant__ FinalParams f) {
   const BwdParams& p = f.b;
@@ -462,13 +477,13 @@ __global__ void __launch_bounds__(32 * kFinalY) norm_bwd_groups_kernel(const __g
   const int start = f.per_group ? 0 : threadIdx.y, step = f.per_group ? 1 : kFinalY;
   float s[kSums] = {0.f, 0.f, 0.f};
   float* base = p.partial + grp * p.chunks * kSums * p.C + c;
+  grid_dependency_wait();
   if (in) {
+#pragma unroll 4
+    for (int i = start; i < p.chunks; i += step) {
+      const volatile float* q = base + (int64_t)i * kSums * p.C;
 #pragma unroll
-    for (int k = 0; k < kSums; ++k) {
-      if (!(p.need & (1 << k))) continue;
-      const float* q = base + (int64_t)k * p.C;
-#pragma unroll 8
-      for (int i = start; i < p.chunks; i += step) s[k] += q[(int64_t)i * kSums * p.C];
+      for (int k = 0; k < kSums; ++k) s[k] += p.need & (1 << k) ? q[(int64_t)k * p.C] : 0.f;
     }
   }
   if (!f.per_group) {
@@ -478,6 +493,7 @@ __global__ void __launch_bounds__(32 * kFinalY) norm_bwd_groups_kernel(const __g
     if (threadIdx.y > 0) return;
 #pragma unroll
     for (int k = 0; k < kSums; ++k)
+#pragma unroll
       for (int y = 1; y < kFinalY; ++y) s[k] += part[k][y][threadIdx.x];
   }
   if (!in) return;
@@ -504,12 +520,13 @@ __global__ void __launch_bounds__(1024) norm_bwd_weights_kernel(const __grid_con
   __shared__ float part[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float* const outs[2] = {p.a.dweight, p.a.dpost_weight};
+  grid_dependency_wait();
   for (int k = 0; k < 2; ++k) {
     if (outs[k] == nullptr) continue;
     float s = 0.f;
     if (c < p.C) {
-      const float* q = p.partial + (int64_t)(k + 1) * p.C + c;
-#pragma unroll 2
+      const volatile float* q = p.partial + (int64_t)(k + 1) * p.C + c;
+#pragma unroll 4
       for (int64_t g = threadIdx.y; g < f.groups; g += 32) s += q[g * p.chunks * kSums * p.C];
     }
     __syncthreads();
@@ -520,6 +537,20 @@ __global__ void __launch_bounds__(1024) norm_bwd_weights_kernel(const __grid_con
       outs[k][c] = s;
     }
   }
+}
+
+// Launch as a programmatic dependent of the kernel before it on the stream.
+cudaError_t launch_dependent(void (*kernel)(FinalParams), dim3 grid, dim3 block, const FinalParams& f, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, f);
 }
 
 template <typename T, int SRC, int POST, bool HALF, int NV, int U, int MAXT>
@@ -609,10 +640,10 @@ cudaError_t launch_norm_bwd(const NormGeom& g, const NormBwdArgs& a, void* works
   if (items > INT32_MAX || group_blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t e = g.bf16 ? launch_type<__nv_bfloat16>(p, (unsigned)items, s) : launch_type<float>(p, (unsigned)items, s);
   if (e != cudaSuccess || p.need == 0) return e;
-  norm_bwd_groups_kernel<<<(unsigned)group_blocks, dim3(32, kFinalY), 0, s>>>(f);
-  if (g.groups > 1 && (a.dweight != nullptr || a.dpost_weight != nullptr))
-    norm_bwd_weights_kernel<<<(g.C + 31) / 32, dim3(32, 32), 0, s>>>(f);
-  return cudaGetLastError();
+  e = launch_dependent(norm_bwd_groups_kernel, dim3((unsigned)group_blocks), dim3(32, kFinalY), f, s);
+  if (e == cudaSuccess && g.groups > 1 && (a.dweight != nullptr || a.dpost_weight != nullptr))
+    e = launch_dependent(norm_bwd_weights_kernel, dim3((g.C + 31) / 32), dim3(32, 32), f, s);
+  return e;
 }
 
 }  // namespace ssta

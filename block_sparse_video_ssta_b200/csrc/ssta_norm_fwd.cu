@@ -97,9 +97,10 @@ __device__ __forceinline__ void save8(const V8& v, const FwdParams& p, const sst
   }
 }
 
+// Eight elements of an optional vector (`other` where it is absent).
 template <typename P>
-__device__ __forceinline__ V8 param8(const void* v, int64_t at, bool in) {
-  return in ? load8(static_cast<const P*>(v) + at) : fill(0.f);
+__device__ __forceinline__ V8 param8(const void* v, int64_t at, bool in, float other) {
+  return v == nullptr ? fill(other) : in ? load8(static_cast<const P*>(v) + at) : fill(0.f);
 }
 
 // NV vectors per lane and row, U rows per thread, LPR lanes and WPR warps per row; POST:
@@ -129,6 +130,21 @@ __global__ void __launch_bounds__(kFwdThreads, !POST ? 3 : sizeof(T) == 2 && WPR
   int64_t mod[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) mod[u] = p.mod_rows < p.rows ? (int64_t)((row0 + u) / p.mod_rows) * p.mod_stride : 0;
+  // A thread with one vector fetches its parameters together with it: few rows are a matter
+  // of latency, and the loads would otherwise start behind each reduction.
+  constexpr bool kEarly = NV * U == 1;
+  V8 early[kEarly ? 5 : 1];
+  if constexpr (kEarly) {
+    const int ch = lane * kVec;
+    const bool in = row0 < p.rows && ch < p.C;
+    early[0] = param8<P>(a.weight, ch, in, 1.f);
+    early[1] = param8<P>(a.scale, mod[0] + ch, in, 0.f);
+    early[2] = param8<P>(a.shift, mod[0] + ch, in, 0.f);
+    if constexpr (POST) {
+      early[3] = param8<P>(a.post_weight, ch, in, 1.f);
+      early[4] = param8<P>(a.gate, mod[0] + ch, in, 1.f);
+    }
+  }
   V8 v[U][NV];
   float mean[U], rstd[U];
   if constexpr (POST) {
@@ -157,7 +173,7 @@ __global__ void __launch_bounds__(kFwdThreads, !POST ? 3 : sizeof(T) == 2 && WPR
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int ch = (i * kRowThreads + lane) * kVec;
-        const V8 w = a.post_weight != nullptr ? param8<P>(a.post_weight, ch, ch < p.C) : fill(1.f);
+        const V8 w = kEarly ? early[kEarly ? 3 : 0] : param8<P>(a.post_weight, ch, ch < p.C, 1.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u][i] = mul(mul(add(v[u][i], fill(-mean[u])), rstd[u]), w);
       }
@@ -168,7 +184,7 @@ __global__ void __launch_bounds__(kFwdThreads, !POST ? 3 : sizeof(T) == 2 && WPR
       for (int i = 0; i < NV; ++i) {
         const int ch = (i * kRowThreads + lane) * kVec;
         const bool in = row0 + u < p.rows && ch < p.C;
-        if (a.gate != nullptr) v[u][i] = mul(v[u][i], param8<P>(a.gate, mod[u] + ch, in));
+        if (a.gate != nullptr) v[u][i] = mul(v[u][i], kEarly ? early[kEarly ? 4 : 0] : param8<P>(a.gate, mod[u] + ch, in, 1.f));
         // products and sum rounded one by one: r does not depend on what gets fused
         v[u][i] = add(mul(unpack(xr[u][i]), p.res_scale), v[u][i]);
         if (!in) v[u][i] = fill(0.f);
@@ -208,42 +224,51 @@ __global__ void __launch_bounds__(kFwdThreads, !POST ? 3 : sizeof(T) == 2 && WPR
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int ch = (i * kRowThreads + lane) * kVec;
-    const V8 w = a.weight != nullptr ? param8<P>(a.weight, ch, ch < p.C) : fill(1.f);
+    const V8 w = kEarly ? early[0] : param8<P>(a.weight, ch, ch < p.C, 1.f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = row0 + u < p.rows && ch < p.C;
       V8 n = mul(add(v[u][i], fill(-mean[u])), rstd[u]);
       if (a.weight != nullptr) n = mul(n, w);
-      if (a.scale != nullptr) n = fma(n, param8<P>(a.scale, mod[u] + ch, in), n);
-      if (a.shift != nullptr) n = add(n, param8<P>(a.shift, mod[u] + ch, in));
+      if (a.scale != nullptr) n = fma(n, kEarly ? early[kEarly ? 1 : 0] : param8<P>(a.scale, mod[u] + ch, in, 0.f), n);
+      if (a.shift != nullptr) n = add(n, kEarly ? early[kEarly ? 2 : 0] : param8<P>(a.shift, mod[u] + ch, in, 0.f));
       if (in) store8(static_cast<T*>(a.n) + base + u * p.C + ch, n);
     }
   }
 }
 
-template <typename T, typename P, int NV, int LPR, int WPR>
-cudaError_t launch_shape(const FwdParams& p, cudaStream_t s) {
-  // four vectors per thread and array; half the rows where two arrays are held
-  constexpr int kU = 4 / NV, kUPost = kU > 1 ? kU / 2 : 1, kSlots = kFwdThreads / (LPR * WPR);
-  if (p.a.y != nullptr) {
-    const unsigned blocks = (p.rows + kSlots * kUPost - 1) / (kSlots * kUPost);
-    norm_fwd_kernel<T, P, NV, kUPost, LPR, WPR, true><<<blocks, kFwdThreads, 0, s>>>(p);
-  } else {
-    const unsigned blocks = (p.rows + kSlots * kU - 1) / (kSlots * kU);
-    norm_fwd_kernel<T, P, NV, kU, LPR, WPR, false><<<blocks, kFwdThreads, 0, s>>>(p);
-  }
+template <typename T, typename P, int NV, int U, int LPR, int WPR, bool POST>
+cudaError_t launch_rows(const FwdParams& p, cudaStream_t s) {
+  constexpr int kRows = kFwdThreads / (LPR * WPR) * U;
+  norm_fwd_kernel<T, P, NV, U, LPR, WPR, POST><<<(p.rows + kRows - 1) / kRows, kFwdThreads, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T, typename P, bool POST>
+cudaError_t launch_shape(const FwdParams& p, cudaStream_t s) {
+  constexpr int kU = POST ? 2 : 4;   // four vectors per thread, of one array or of two
+  if (p.C <= 128) return launch_rows<T, P, 1, kU, 16, 1, POST>(p, s);
+  if (p.C <= 256) return launch_rows<T, P, 1, kU, 32, 1, POST>(p, s);
+  // Few rows, all of them resident at once with a vector per thread (two blocks of 256
+  // threads per SM): 256 x 2048 takes 7.7 us with four vectors per thread.
+  if (p.C <= 2048) {
+    const int warps = p.C <= 512 ? 2 : p.C <= 1024 ? 4 : 8;
+    if ((int64_t)p.rows * warps <= 148 * 2 * (kFwdThreads / 32)) {
+      if (warps == 2) return launch_rows<T, P, 1, 1, 32, 2, POST>(p, s);
+      if (warps == 4) return launch_rows<T, P, 1, 1, 32, 4, POST>(p, s);
+      return launch_rows<T, P, 1, 1, 32, 8, POST>(p, s);
+    }
+  }
+  if (p.C <= 512) return launch_rows<T, P, 2, kU / 2, 32, 1, POST>(p, s);
+  if (p.C <= 1024) return launch_rows<T, P, 4, 1, 32, 1, POST>(p, s);
+  if (p.C <= 2048) return launch_rows<T, P, 4, 1, 32, 2, POST>(p, s);
+  if (p.C <= 4096) return launch_rows<T, P, 4, 1, 32, 4, POST>(p, s);
+  return launch_rows<T, P, 4, 1, 32, 8, POST>(p, s);
 }
 
 template <typename T, typename P>
 cudaError_t launch_types(const FwdParams& p, cudaStream_t s) {
-  if (p.C <= 128) return launch_shape<T, P, 1, 16, 1>(p, s);
-  if (p.C <= 256) return launch_shape<T, P, 1, 32, 1>(p, s);
-  if (p.C <= 512) return launch_shape<T, P, 2, 32, 1>(p, s);
-  if (p.C <= 1024) return launch_shape<T, P, 4, 32, 1>(p, s);
-  if (p.C <= 2048) return launch_shape<T, P, 4, 32, 2>(p, s);
-  if (p.C <= 4096) return launch_shape<T, P, 4, 32, 4>(p, s);
-  return launch_shape<T, P, 4, 32, 8>(p, s);
+  return p.a.y != nullptr ? launch_shape<T, P, true>(p, s) : launch_shape<T, P, false>(p, s);
 }
 
 }  // namespace

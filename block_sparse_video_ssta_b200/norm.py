@@ -15,7 +15,9 @@ and its outputs' readers behind it as for any work on that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -95,6 +97,12 @@ def ssta_norm_plan(desc: NormDesc) -> NormPlan:
     return NormPlan(info.groups, info.exponents_per_row, info.bwd_workspace_bytes)
 
 
+@functools.lru_cache(maxsize=256)
+def _bwd_bytes(rows, C, mod_rows):
+    """Workspace of the backwards (no other field of a descriptor changes it)."""
+    return ssta_norm_plan(norm_desc(rows, C, mod_rows=mod_rows)).bwd_workspace_bytes
+
+
 class Checkpoint:
     """An activation kept in 8 bits: ``codes`` [..., C] (torch.int8 or torch.float8_e4m3fn), ``exponents``
     [..., ceil(C / 128)] (torch.uint8), and the ``dtype`` its values are read as.  The value of a code is
@@ -113,6 +121,9 @@ class Checkpoint:
         _ptr(exponents, "exponents", torch.uint8, want)
         if exponents.device != codes.device:
             raise ValueError(f"exponents are on {exponents.device}, codes on {codes.device}")
+        self._set(codes, exponents, dtype)
+
+    def _set(self, codes, exponents, dtype):
         self.codes, self.exponents, self.dtype = codes, exponents, dtype
         self._c = _Ckpt(codes.data_ptr(), exponents.data_ptr(), FORMATS[_CODE_NAMES[codes.dtype]])
 
@@ -137,9 +148,13 @@ class Checkpoint:
         """An unwritten checkpoint of a tensor of this shape."""
         if format not in _CODE_DTYPES:
             raise ValueError(f"format {format!r}, expected one of {sorted(_CODE_DTYPES)}")
+        if dtype not in _VALUE_DTYPES:
+            raise ValueError(f"values have dtype {dtype}, expected torch.bfloat16 or torch.float32")
         shape = tuple(shape)
-        return cls(torch.empty(shape, dtype=_CODE_DTYPES[format], device=device),
-                   torch.empty(shape[:-1] + (-(-shape[-1] // GROUP),), dtype=torch.uint8, device=device), dtype)
+        ckpt = cls.__new__(cls)
+        ckpt._set(torch.empty(shape, dtype=_CODE_DTYPES[format], device=device),
+                  torch.empty(shape[:-1] + (-(-shape[-1] // GROUP),), dtype=torch.uint8, device=device), dtype)
+        return ckpt
 
 
 @dataclass
@@ -179,10 +194,13 @@ class ResidualNormGrads:
     workspace: torch.Tensor
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(stream, dev):
     """Context in which `dev` and the call's stream are current."""
     if stream is None:
-        return torch.cuda.device(dev)
+        return _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
     if stream.device != dev:
@@ -191,7 +209,8 @@ def _on(stream, dev):
 
 
 def _current(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+    # the raw handle: torch.cuda.current_stream builds a Stream object, a fifth of a small call
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _device(t, name):
@@ -202,28 +221,38 @@ def _device(t, name):
 
 class _Args:
     """Checks one call's tensors against its descriptor and returns their addresses."""
+    __slots__ = ("desc", "dev", "index", "rows", "C", "n", "dtype", "param", "groups")
 
     def __init__(self, desc: NormDesc, dev):
-        self.desc, self.dev = desc, dev
+        self.desc, self.dev, self.index = desc, dev, dev.index
         self.rows, self.C = desc.rows, desc.C
+        self.n = self.rows * self.C
         self.dtype = torch.bfloat16 if desc.dtype == SSTA_BF16 else torch.float32
         self.param = torch.bfloat16 if desc.param_dtype == SSTA_BF16 else torch.float32
-        self.groups = -(-self.rows // min(desc.mod_rows or self.rows, self.rows))
+        m = desc.mod_rows
+        self.groups = 1 if m == 0 or m >= self.rows else -(-self.rows // m)
 
     def _dense(self, t, name, dtype, numel, last):
+        try:
+            if t.dtype is dtype and t.get_device() == self.index and t.numel() == numel and t.is_contiguous() and (
+                    not last or t.shape[-1] == last):
+                return t.data_ptr()
+        except (AttributeError, IndexError):
+            pass
+        self._refuse(t, name, dtype, numel, last)
+
+    def _refuse(self, t, name, dtype, numel, last):
         if not isinstance(t, torch.Tensor) or t.device != self.dev:
             raise ValueError(f"{name} must be a tensor on {self.dev}")
         if t.dtype != dtype:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if t.numel() != numel or (last and (t.dim() < 1 or t.shape[-1] != last)):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {numel // last if last else numel} rows"
-                             + (f" of {last}" if last else ""))
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {numel // last if last else numel} "
+                         + (f"rows of {last}" if last else "elements"))
 
     def act(self, t, name):
-        return None if t is None else self._dense(t, name, self.dtype, self.rows * self.C, self.C)
+        return None if t is None else self._dense(t, name, self.dtype, self.n, self.C)
 
     def weight(self, t, name):
         return None if t is None else self._dense(t, name, self.param, self.C, self.C)
@@ -237,20 +266,22 @@ class _Args:
     def mod(self, t, name):
         if t is None:
             return None
-        if not isinstance(t, torch.Tensor) or t.device != self.dev:
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
             raise ValueError(f"{name} must be a tensor on {self.dev}")
-        if t.dtype != self.param:
+        if t.dtype is not self.param:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {self.param}")
-        if t.dim() < 1 or t.shape[-1] != self.C or t.numel() != self.groups * self.C:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.groups} rows of {self.C}")
-        if t.stride(-1) != 1:
+        shape, strides = t.shape, t.stride()
+        if not shape or shape[-1] != self.C or t.numel() != self.groups * self.C:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected {self.groups} rows of {self.C}")
+        if strides[-1] != 1:
             raise ValueError(f"{name} must have contiguous channels")
-        want = self.desc.mod_stride or self.C
-        for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-            if size != 1:
-                if stride != want:
-                    raise ValueError(f"{name} has row stride {stride}, expected {want} (the descriptor's mod_stride)")
-                want *= size
+        if self.groups > 1:
+            want = self.desc.mod_stride or self.C
+            for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+                if size != 1:
+                    if stride != want:
+                        raise ValueError(f"{name} has row stride {stride}, expected {want} (the descriptor's mod_stride)")
+                    want *= size
         return t.data_ptr()
 
     def kept(self, t, name):
@@ -259,7 +290,7 @@ class _Args:
             return self.act(t, name), None
         if t.device != self.dev:
             raise ValueError(f"{name} must be a checkpoint on {self.dev}")
-        if t.codes.numel() != self.rows * self.C or t.shape[-1] != self.C:
+        if t.codes.numel() != self.n or t.shape[-1] != self.C:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.rows} rows of {self.C}")
         return None, ctypes.byref(t._c)
 
@@ -277,14 +308,15 @@ class _Args:
         return want
 
     def new_act(self, t, like):
-        return torch.empty(like.shape, dtype=self.dtype, device=self.dev) if t is None else t
+        """An output shaped like a checked activation."""
+        return torch.empty_like(like) if t is None else t
 
     def new_f32(self, t, *shape):
         return torch.empty(shape, dtype=torch.float32, device=self.dev) if t is None else t
 
     def workspace(self, t):
         if t is None:
-            t = _workspace(ssta_norm_plan(self.desc).bwd_workspace_bytes, self.dev)
+            t = _workspace(_bwd_bytes(self.rows, self.C, self.desc.mod_rows), self.dev)
         return t, self._dense(t, "workspace", torch.uint8, t.numel(), 0)
 
 
