@@ -1,4 +1,4 @@
-"""Python binding of libssta.so, the SSTA forward library for B200 (sm_100a).
+"""Python binding of libssta.so, the SSTA library for B200 (sm_100a).
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  The functions carry the C entry points' names (include/ssta.h) and
@@ -19,7 +19,7 @@ import torch
 __all__ = [
     "SstaError", "SSTA_BF16", "SSTA_F32", "Desc", "desc_from", "ssta_plan", "ssta_tile_reorder",
     "ssta_build_block_mask", "ssta_attention_fwd", "ssta_attention_bwd", "ssta_tile_unorder", "ssta_read_device_status",
-    "ssta_status_string", "ssta_forward", "library_path", "lib",
+    "ssta_status_string", "ssta_forward", "ssta_backward", "SstaSaved", "library_path", "lib",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -303,23 +303,94 @@ def ssta_read_device_status(workspace, stream=None) -> int:
     return int(code.value)
 
 
-def ssta_forward(desc: Desc, q, k, v, q_text=None, k_text=None, v_text=None, stream=None, tile_scores=None):
+def ssta_forward(desc: Desc, q, k, v, q_text=None, k_text=None, v_text=None, stream=None, tile_scores=None,
+                 q_weight=None, k_weight=None, norm_eps=1e-6, checkpoint=None):
     """The whole SSTA forward: reorder q, k, v; build the block mask; attend; unorder O.
 
     Returns a dict with O (raster), O_text, and the intermediate packed tensors,
     lists, LSE and workspaces.
+
+    ``q_weight``, ``k_weight`` [D] (bf16 or f32): RMS-normalise every head's q and k (video
+    and text) with these weights first.  ``checkpoint``: None, "int8" or "e4m3"; with a
+    format, what ssta_backward reads is kept as 8-bit checkpoints and the packed tensors
+    are not returned (qp, kp, vp and O_packed are None).  ``saved`` in the result is
+    ssta_backward's argument.
     """
-    qp = ssta_tile_reorder(desc, q, q_text, stream=stream)
-    kp = ssta_tile_reorder(desc, k, k_text, stream=stream)
-    vp = ssta_tile_reorder(desc, v, v_text, stream=stream)
+    if q_weight is None and k_weight is None and checkpoint is None:
+        qp = ssta_tile_reorder(desc, q, q_text, stream=stream)
+        kp = ssta_tile_reorder(desc, k, k_text, stream=stream)
+        vp = ssta_tile_reorder(desc, v, v_text, stream=stream)
+        return _attend(desc, qp, kp, vp, stream, tile_scores)
+    with _on(stream, q.device):   # packed tensors dropped below go back to the stream that used them
+        packed, norms = [], []
+        for x, x_text, weight in ((q, q_text, q_weight), (k, k_text, k_weight), (v, v_text, None)):
+            p = ssta_tile_reorder(desc, x, x_text)
+            if weight is not None:
+                # pad rows are zeros and stay so
+                nd = norm_desc(p.numel() // desc.D, desc.D, desc.dtype, _VALUE_DTYPES[weight.dtype], "rms", eps=norm_eps)
+                y, _, rstd, kept = ssta_norm_fwd(nd, p, weight, y=p if checkpoint else None, save=checkpoint)
+                norms.append((nd, kept if checkpoint else p, rstd, weight))
+                p = y
+            elif x is not v:
+                norms.append(None)
+            packed.append(p)
+        r = _attend(desc, *packed, None, tile_scores)
+        r["saved"].norms = tuple(norms)
+        if checkpoint is not None:
+            names = ("qp", "kp", "vp", "O_packed")
+            r["saved"].q, r["saved"].k, r["saved"].v, r["saved"].o = (ssta_checkpoint_save(r[n], checkpoint) for n in names)
+            r.update(dict.fromkeys(names))
+        return r
+
+
+def _attend(desc, qp, kp, vp, stream, tile_scores):
     kv_idx, kv_cnt, ws_mask = ssta_build_block_mask(desc, qp, kp, tile_scores=tile_scores, stream=stream)
     op, lse, ws_attn = ssta_attention_fwd(desc, qp, kp, vp, kv_idx, kv_cnt, stream=stream)
     o, o_text = ssta_tile_unorder(desc, op, stream=stream)
     return dict(O=o, O_text=o_text, qp=qp, kp=kp, vp=vp, kv_idx=kv_idx, kv_cnt=kv_cnt, O_packed=op, LSE=lse,
-                ws_mask=ws_mask, ws_attn=ws_attn)
+                ws_mask=ws_mask, ws_attn=ws_attn, saved=SstaSaved(qp, kp, vp, op, lse, kv_idx, kv_cnt))
+
+
+@dataclass
+class SstaSaved:
+    """What ssta_backward reads: the packed q, k, v and O (tensors, or Checkpoints), LSE, the kept lists, and for q
+    and k the head norm's (descriptor, input, rstd, weight), None where there is no norm."""
+    q: object
+    k: object
+    v: object
+    o: object
+    lse: torch.Tensor
+    kv_idx: torch.Tensor
+    kv_cnt: torch.Tensor
+    norms: tuple = (None, None)
+
+
+def ssta_backward(desc: Desc, saved: SstaSaved, dO, dO_text=None, stream=None):
+    """The whole SSTA backward, from the gradients of ssta_forward's O [B,H,T,Y,X,D] and O_text [B,H,L,D].
+
+    ``saved``: ``ssta_forward(...)["saved"]``.  The kept lists are constants: no gradient
+    passes through the selection.  Returns a dict with dq, dk, dv (raster), dq_text, dk_text,
+    dv_text (None without text), dq_weight, dk_weight ([D] float32, None without head norms)
+    and the attention backward's workspace (ssta_read_device_status)."""
+    with _on(stream, dO.device):
+        do = ssta_tile_reorder(desc, dO, dO_text)
+        rest = (saved.lse, do, saved.kv_idx, saved.kv_cnt)
+        if isinstance(saved.q, Checkpoint):
+            *grads, ws = ssta_attention_bwd_checkpoint(desc, saved.q, saved.k, saved.v, saved.o, *rest)
+        else:
+            *grads, ws = ssta_attention_bwd(desc, saved.q, saved.k, saved.v, saved.o, saved.lse, *rest[1:])
+        out = dict(workspace=ws)
+        for name, g, norm in zip(("q", "k", "v"), grads, saved.norms + (None,)):
+            if norm is not None:
+                nd, x, rstd, weight = norm
+                out[f"d{name}_weight"] = ssta_norm_bwd(nd, g, x, None, rstd, weight, dx=g).dweight
+            elif name != "v":
+                out[f"d{name}_weight"] = None
+            out[f"d{name}"], out[f"d{name}_text"] = ssta_tile_unorder(desc, g)
+    return out
 
 
 from .norm import *  # noqa: E402,F401,F403  (needs the names above)
-from .norm import __all__ as _norm_all  # noqa: E402
+from .norm import _VALUE_DTYPES, _on, __all__ as _norm_all  # noqa: E402
 
 __all__ += _norm_all

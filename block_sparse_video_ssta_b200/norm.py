@@ -311,8 +311,10 @@ class _Args:
         """An output shaped like a checked activation."""
         return torch.empty_like(like) if t is None else t
 
-    def new_f32(self, t, *shape):
-        return torch.empty(shape, dtype=torch.float32, device=self.dev) if t is None else t
+    def new_f32(self, t, *shape, like=None):
+        if t is not None:
+            return t
+        return torch.empty(shape, dtype=torch.float32, device=self.dev) if like is None else torch.empty_like(like)
 
     def workspace(self, t):
         if t is None:
@@ -337,7 +339,7 @@ def ssta_norm_fwd(desc: NormDesc, x, weight=None, scale=None, shift=None, y=None
         y = a.new_act(y, x)
         if stats:
             mean = a.new_f32(mean, a.rows) if desc.norm == 1 else mean
-            rstd = a.new_f32(rstd, a.rows)
+            rstd = a.new_f32(rstd, a.rows, like=mean)
         saved = a.save(save, x, "save")
         _check(lib.ssta_norm_fwd(
             ctypes.byref(desc), px, a.weight(weight, "weight"), a.mod(scale, "scale"), a.mod(shift, "shift"),
@@ -359,7 +361,7 @@ def ssta_norm_bwd(desc: NormDesc, dy, x, mean, rstd, weight=None, scale=None, dr
         dweight = a.new_f32(dweight, a.C) if weight is not None else dweight
         dscale = a.new_f32(dscale, a.groups, a.C) if scale is not None else dscale
         if want_dshift if want_dshift is not None else scale is not None:
-            dshift = a.new_f32(dshift, a.groups, a.C)
+            dshift = a.new_f32(dshift, a.groups, a.C, like=dscale)
         workspace, pw = a.workspace(workspace)
         _check(lib.ssta_norm_bwd(
             ctypes.byref(desc), pdy, px, cx, a.stat(mean, "mean"), a.stat(rstd, "rstd"), a.weight(weight, "weight"),
@@ -381,9 +383,11 @@ def ssta_residual_norm_fwd(desc: NormDesc, x, y, post_weight=None, gate=None, we
         px, py = a.act(x, "x"), a.act(y, "y")
         r = a.new_act(r, x)
         n = a.new_act(n, x) if desc.norm != 0 else n
-        stat = lambda on: a.new_f32(None, a.rows) if stats and on else None
-        pm, pr = stat(desc.post_norm == 1), stat(desc.post_norm != 0)
-        m, rs = stat(desc.norm == 1), stat(desc.norm != 0)
+        stat = lambda on, like=None: a.new_f32(None, a.rows, like=like) if stats and on else None
+        pr = stat(desc.post_norm != 0)
+        pm = stat(desc.post_norm == 1, pr)
+        rs = stat(desc.norm != 0, pr)
+        m = stat(desc.norm == 1, rs)
         cy, cr = a.save(save_y, y, "save_y"), a.save(save_r, x, "save_r")
         _check(lib.ssta_residual_norm_fwd(
             ctypes.byref(desc), px, py, a.weight(post_weight, "post_weight"), a.mod(gate, "gate"),
@@ -413,7 +417,7 @@ def ssta_residual_norm_bwd(desc: NormDesc, dr, dn, r=None, y=None, mean=None, rs
             dweight = a.new_f32(dweight, a.C) if weight is not None else dweight
             dscale = a.new_f32(dscale, a.groups, a.C) if scale is not None else dscale
             if want_dshift if want_dshift is not None else scale is not None:
-                dshift = a.new_f32(dshift, a.groups, a.C)
+                dshift = a.new_f32(dshift, a.groups, a.C, like=dscale)
         workspace, pw = a.workspace(workspace)
         _check(lib.ssta_residual_norm_bwd(
             ctypes.byref(desc), a.act(dr, "dr"), a.act(dn, "dn"), pr_, cr, py, cy, a.stat(post_mean, "post_mean"),
