@@ -15,9 +15,9 @@
 //                         that keep it (one warp per key tile: a binary search
 //                         in every query tile's sorted list, ballots, prefix).
 //   bwd_dq_kernel         one warp per query row, walking its tile's kept list
-//                         (fp32; bf16 runs bwd_dq_tc_kernel on the tensor cores).
+//                         (fp32; bf16 runs bwd_tc_kernel on the tensor cores).
 //   bwd_dkdv_kernel       one warp per key row, walking the transposed list
-//                         (fp32; bf16 runs bwd_dkdv_tc_kernel on the tensor cores).
+//                         (fp32; bf16: the same bwd_tc_kernel).
 // The SIMT kernels (fp32 storage) use fp32 arithmetic, one lane per four
 // channels; for bf16 every product runs on the tensor cores
 // (ssta_attn_bwd_tc.cu).
@@ -276,9 +276,8 @@ cudaError_t launch_bwd_typed(const Geom& g, const void* q, const void* k, const 
   }
   bwd_transpose_kernel<<<tb, kBwdWarps * 32, 0, s>>>(g, kv_idx, kv_cnt, tidx, tcnt, status);
   if constexpr (kTensorCores<T>) {   // bf16: the API guarantees N % 128 == 0
-    cudaError_t e = launch_attention_bwd_dq_tc(g, q, k, v, dO, lse, Dv, kv_idx, kv_cnt, dq, status, s);
-    if (e != cudaSuccess) return e;
-    e = launch_attention_bwd_dkdv_tc(g, q, k, v, dO, nl2, nd, tidx, tcnt, dk, dv, status, s);
+    const cudaError_t e = launch_attention_bwd_tc(g, q, k, v, dO, lse, Dv, nl2, nd, kv_idx, kv_cnt, tidx, tcnt, dq, dk,
+                                                  dv, status, s);
     if (e != cudaSuccess) return e;
   } else {
     bwd_dq_kernel<T><<<rb, kBwdWarps * 32, 0, s>>>(g, tq, tk, tv, tO, lse, Dv, kv_idx, kv_cnt, static_cast<T*>(dq),

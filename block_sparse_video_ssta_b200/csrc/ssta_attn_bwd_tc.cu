@@ -64,12 +64,12 @@ enum : int {
 // columns 16 kk .. 16 kk + 15:
 __device__ __forceinline__ uint32_t pcol(int kk) { return 8u * (uint32_t)kk + ((uint32_t)(kk >> 2) << 5); }
 
-__global__ void __launch_bounds__(kDqThreads, 1)
-bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO, const Geom g,
-                 const __grid_constant__ ChunkTables tb, const int32_t* __restrict__ kv_idx, const int32_t* __restrict__ kv_cnt,
-                 const float* __restrict__ lse, const float* __restrict__ Dv, __nv_bfloat16* __restrict__ dq,
-                 int32_t* __restrict__ status, float scale_log2) {
+// dQ of work unit `u`, by one CTA.
+__device__ __forceinline__ void
+dq_unit(int64_t u, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmDO,
+        const Geom& g, const ChunkTables& tb, const int32_t* __restrict__ kv_idx, const int32_t* __restrict__ kv_cnt,
+        const float* __restrict__ lse, const float* __restrict__ Dv, __nv_bfloat16* __restrict__ dq,
+        int32_t* __restrict__ status, float scale_log2) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -86,7 +86,6 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const int blocks = g.N / 128;
   const int64_t BH = (int64_t)g.B * g.H;
   const int64_t text_units = BH * g.n_text * blocks;
-  int64_t u = blockIdx.x;
   int64_t bh;
   int qt, blk;
   if (u < text_units) {
@@ -429,31 +428,6 @@ cudaError_t launch_attention_bwd_rowstat_tc(const Geom& g, const void* o, const 
   return cudaGetLastError();
 }
 
-cudaError_t launch_attention_bwd_dq_tc(const Geom& g, const void* q, const void* k, const void* v, const void* dO,
-                                       const float* lse, const float* Dv, const int32_t* kv_idx,
-                                       const int32_t* kv_cnt, void* dq, int32_t* status, cudaStream_t s) {
-  const int64_t BH = (int64_t)g.B * g.H;
-  if (BH == 0) return cudaSuccess;
-  CUtensorMap mq, mk, mv, mdo;
-  if (!make_map(&mq, q, g) || !make_map(&mk, k, g) || !make_map(&mv, v, g) || !make_map(&mdo, dO, g))
-    return cudaErrorInvalidValue;
-  static std::atomic<bool> attr_set[64];
-  int dev = -1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(bwd_dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemAlloc);
-    if (e != cudaSuccess) return e;
-    attr_set[dev].store(true, std::memory_order_release);
-  }
-  const int64_t units = BH * (int64_t)g.NQ * (g.N / 128);
-  bwd_dq_tc_kernel<<<(unsigned)units, kDqThreads, kSmemAlloc, s>>>(mq, mk, mv, mdo, g, make_chunk_tables(g), kv_idx,
-                                                                   kv_cnt, lse, Dv, static_cast<__nv_bfloat16*>(dq),
-                                                                   status, g.scale * 1.4426950408889634f);
-  return cudaGetLastError();
-}
-
 // ============================================================================
 // dK and dV on the tensor cores:  dV = P^T dO,  dK = scale * dS^T Q, for one
 // 128-key block, summed over the 128-row query chunks of every query tile that
@@ -533,12 +507,12 @@ __device__ __forceinline__ int for_each_qchunk(const Geom& g, const ChunkTables&
   return step;
 }
 
-__global__ void __launch_bounds__(kKvThreads, 1)
-bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO, const Geom g,
-                   const __grid_constant__ ChunkTables tb, const int32_t* __restrict__ tidx, const int32_t* __restrict__ tcnt,
-                   const float* __restrict__ nl2, const float* __restrict__ nd, __nv_bfloat16* __restrict__ dk,
-                   __nv_bfloat16* __restrict__ dv, int32_t* __restrict__ status, float scale_log2) {
+// dK and dV of work unit `u`, by one CTA.
+__device__ __forceinline__ void
+dkdv_unit(int64_t u, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmDO,
+          const Geom& g, const ChunkTables& tb, const int32_t* __restrict__ tidx, const int32_t* __restrict__ tcnt,
+          const float* __restrict__ nl2, const float* __restrict__ nd, __nv_bfloat16* __restrict__ dk,
+          __nv_bfloat16* __restrict__ dv, int32_t* __restrict__ status, float scale_log2) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -563,7 +537,6 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const int blocks = g.N / 128;
   const int64_t BH = (int64_t)g.B * g.H;
   const int64_t text_units = BH * g.n_text * blocks;
-  int64_t u = blockIdx.x;
   int64_t bh;
   int kt, blk;
   if (u < text_units) {
@@ -823,11 +796,34 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   }
 }
 
+// Both halves of the backward in one grid: first the dK/dV units, which take longer, then
+// the dQ units.  They are independent, and a problem smaller than the GPU then takes the
+// longer of the two instead of their sum (one CTA per SM either way: each takes all of an
+// SM's tensor memory and most of its shared memory).
+static_assert(kDqThreads == kKvThreads && kSmemAlloc <= kKvSmemAlloc, "one launch serves both");
+
+__global__ void __launch_bounds__(kKvThreads, 1)
+bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+              const __grid_constant__ Geom g, const __grid_constant__ ChunkTables tb, int64_t units,
+              const int32_t* __restrict__ kv_idx, const int32_t* __restrict__ kv_cnt,
+              const int32_t* __restrict__ tidx, const int32_t* __restrict__ tcnt, const float* __restrict__ lse,
+              const float* __restrict__ Dv, const float* __restrict__ nl2, const float* __restrict__ nd,
+              __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+              int32_t* __restrict__ status, float scale_log2) {
+  if ((int64_t)blockIdx.x < units)
+    dkdv_unit(blockIdx.x, tmQ, tmK, tmV, tmDO, g, tb, tidx, tcnt, nl2, nd, dk, dv, status, scale_log2);
+  else
+    dq_unit(blockIdx.x - units, tmQ, tmK, tmV, tmDO, g, tb, kv_idx, kv_cnt, lse, Dv, dq, status, scale_log2);
+}
+
 }  // namespace
 
-cudaError_t launch_attention_bwd_dkdv_tc(const Geom& g, const void* q, const void* k, const void* v, const void* dO,
-                                         const float* nl2, const float* nd, const int32_t* tidx,
-                                         const int32_t* tcnt, void* dk, void* dv, int32_t* status, cudaStream_t s) {
+cudaError_t launch_attention_bwd_tc(const Geom& g, const void* q, const void* k, const void* v, const void* dO,
+                                    const float* lse, const float* Dv, const float* nl2, const float* nd,
+                                    const int32_t* kv_idx, const int32_t* kv_cnt, const int32_t* tidx,
+                                    const int32_t* tcnt, void* dq, void* dk, void* dv, int32_t* status,
+                                    cudaStream_t s) {
   const int64_t BH = (int64_t)g.B * g.H;
   if (BH == 0) return cudaSuccess;
   CUtensorMap mq, mk, mv, mdo;
@@ -839,14 +835,15 @@ cudaError_t launch_attention_bwd_dkdv_tc(const Geom& g, const void* q, const voi
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(bwd_dkdv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKvSmemAlloc);
+    e = cudaFuncSetAttribute(bwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKvSmemAlloc);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
   const int64_t units = BH * (int64_t)g.NQ * (g.N / 128);
-  bwd_dkdv_tc_kernel<<<(unsigned)units, kKvThreads, kKvSmemAlloc, s>>>(
-      mq, mk, mv, mdo, g, make_chunk_tables(g), tidx, tcnt, nl2, nd, static_cast<__nv_bfloat16*>(dk),
-      static_cast<__nv_bfloat16*>(dv), status, g.scale * 1.4426950408889634f);
+  bwd_tc_kernel<<<(unsigned)(2 * units), kKvThreads, kKvSmemAlloc, s>>>(
+      mq, mk, mv, mdo, g, make_chunk_tables(g), units, kv_idx, kv_cnt, tidx, tcnt, lse, Dv, nl2, nd,
+      static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), status,
+      g.scale * 1.4426950408889634f);
   return cudaGetLastError();
 }
 

@@ -100,17 +100,16 @@ cudaError_t launch_attention_bwd(const Geom& g, const void* q, const void* k, co
                                  const ssta_checkpoint* o_saved, const float* lse, const void* dO,
                                  const int32_t* kv_idx, const int32_t* kv_cnt, void* dq, void* dk, void* dv,
                                  void* workspace, cudaStream_t s);
-// bf16, N % 128 == 0: dQ on the tensor cores (Dv = rowsum(dO * O) already computed).
-cudaError_t launch_attention_bwd_dq_tc(const Geom& g, const void* q, const void* k, const void* v, const void* dO,
-                                       const float* lse, const float* Dv, const int32_t* kv_idx,
-                                       const int32_t* kv_cnt, void* dq, int32_t* status, cudaStream_t s);
-// bf16, N % 128 == 0: dK and dV on the tensor cores (tidx/tcnt: the transposed lists).
+// bf16, N % 128 == 0: row statistics for the tensor-core kernel, and dQ, dK and dV in one
+// grid (Dv = rowsum(dO * O); tidx/tcnt: the transposed lists).
 cudaError_t launch_attention_bwd_rowstat_tc(const Geom& g, const void* o, const ssta_checkpoint* o_saved,
                                             const void* dO, const float* lse, float* Dv, float* nl2, float* nd,
                                             cudaStream_t s);
-cudaError_t launch_attention_bwd_dkdv_tc(const Geom& g, const void* q, const void* k, const void* v, const void* dO,
-                                         const float* nl2, const float* nd, const int32_t* tidx,
-                                         const int32_t* tcnt, void* dk, void* dv, int32_t* status, cudaStream_t s);
+cudaError_t launch_attention_bwd_tc(const Geom& g, const void* q, const void* k, const void* v, const void* dO,
+                                    const float* lse, const float* Dv, const float* nl2, const float* nd,
+                                    const int32_t* kv_idx, const int32_t* kv_cnt, const int32_t* tidx,
+                                    const int32_t* tcnt, void* dq, void* dk, void* dv, int32_t* status,
+                                    cudaStream_t s);
 cudaError_t launch_attention_bf16_tc(const Geom& g, const void* qp, const void* kp, const void* vp,
                                      const int32_t* kv_idx, const int32_t* kv_cnt, void* o, float* lse,
                                      int32_t* status, cudaStream_t s);
