@@ -14,8 +14,8 @@
 // are in flight per thread without registers and without a barrier (channels and rows
 // that do not exist are filled with zeros there, so the arithmetic has no conditions).
 // r and y may be 8-bit checkpoints: their codes are what is copied, and they are decoded
-// on the way to registers, which saves one of the two bytes of a bf16 read.  Two small
-// kernels add the runs' sums in a fixed order (no atomics: equal inputs give equal bytes).
+// on the way to registers, which saves one of the two bytes of a bf16 read.  A small
+// kernel adds the runs' sums in a fixed order (no atomics: equal inputs give equal bytes).
 //
 // What bounds it: HBM, once the instructions fit.  A thread handles two rows at a time
 // (bf16) and works on pairs of channels; the row sums of both rows share one butterfly,
@@ -451,52 +451,33 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   }
 }
 
-// Sums of the runs of each group, in order, and the modulation's gradients from them;
-// leaves the group's term of dweight and dpost_weight in its first run's place (or, with
-// one group, writes the gradient).  32 channels per block; 16 threads per channel share a
-// group's runs, or take a group each where a group has few runs.  Launched as a
-// programmatic dependent of the kernel before: only its launch overlaps that kernel.
-constexpr int kFinalY = 16;
+// The runs' sums, added in a fixed order, and every vector's gradient from them.  32
+// channels per block.  Launched as programmatic dependents of the kernel before: only their
+// launch overlaps it.
 struct FinalParams {
   BwdParams b;
   uint32_t groups;
   int channel_blocks;
-  bool per_group;   // a group per thread row
+  int slices;   // warps that share a group's runs
 };
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-__global__ void __launch_bounds__(32 * kFinalY) norm_bwd_groups_kernel(const __grid_constant__ FinalParams f) {
-  const BwdParams& p = f.b;
-  const NormBwdArgs& a = p.a;
-  __shared__ float part[kSums][kFinalY][32];
-  const int c = (blockIdx.x % f.channel_blocks) * 32 + threadIdx.x;
-  const uint32_t gb = blockIdx.x / f.channel_blocks;
-  const int64_t grp = f.per_group ? (int64_t)gb * kFinalY + threadIdx.y : gb;
-  const bool in = c < p.C && grp < f.groups;
-  const int start = f.per_group ? 0 : threadIdx.y, step = f.per_group ? 1 : kFinalY;
-  float s[kSums] = {0.f, 0.f, 0.f};
-  float* base = p.partial + grp * p.chunks * kSums * p.C + c;
-  grid_dependency_wait();
-  if (in) {
+// Sum of every `step`th run from `start` of group `grp`, channel c.
+__device__ __forceinline__ void sum_runs(const BwdParams& p, int64_t grp, int c, int start, int step, float (&s)[kSums]) {
+  const volatile float* base = p.partial + grp * p.chunks * kSums * p.C + c;
 #pragma unroll 4
-    for (int i = start; i < p.chunks; i += step) {
-      const volatile float* q = base + (int64_t)i * kSums * p.C;
+  for (int i = start; i < p.chunks; i += step) {
+    const volatile float* q = base + (int64_t)i * kSums * p.C;
 #pragma unroll
-      for (int k = 0; k < kSums; ++k) s[k] += p.need & (1 << k) ? q[(int64_t)k * p.C] : 0.f;
-    }
+    for (int k = 0; k < kSums; ++k) s[k] += p.need & (1 << k) ? q[(int64_t)k * p.C] : 0.f;
   }
-  if (!f.per_group) {
-#pragma unroll
-    for (int k = 0; k < kSums; ++k) part[k][threadIdx.y][threadIdx.x] = s[k];
-    __syncthreads();
-    if (threadIdx.y > 0) return;
-#pragma unroll
-    for (int k = 0; k < kSums; ++k)
-#pragma unroll
-      for (int y = 1; y < kFinalY; ++y) s[k] += part[k][y][threadIdx.x];
-  }
-  if (!in) return;
+}
+
+// Writes the modulation's gradients of one group and channel from its sums; returns its
+// terms of dweight and dpost_weight.
+__device__ __forceinline__ float2 finish_group(const BwdParams& p, int64_t grp, int c, const float (&s)[kSums]) {
+  const NormBwdArgs& a = p.a;
   auto param = [&](const void* v, int64_t i) {
     return p.param_f32 ? static_cast<const float*>(v)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(v)[i]);
   };
@@ -504,17 +485,69 @@ __global__ void __launch_bounds__(32 * kFinalY) norm_bwd_groups_kernel(const __g
   if (a.dshift != nullptr) a.dshift[out] = s[0];
   if (a.dscale != nullptr) a.dscale[out] = a.weight != nullptr ? s[1] * param(a.weight, c) : s[1];
   if (a.dgate != nullptr) a.dgate[out] = a.post_weight != nullptr ? s[2] * param(a.post_weight, c) : s[2];
-  if (a.dweight != nullptr) {
-    const float t = a.scale != nullptr ? fmaf(s[1], param(a.scale, mod), s[1]) : s[1];
-    if (f.groups == 1) a.dweight[c] = t; else base[p.C] = t;
+  float2 t = make_float2(0.f, 0.f);
+  if (a.dweight != nullptr) t.x = a.scale != nullptr ? fmaf(s[1], param(a.scale, mod), s[1]) : s[1];
+  if (a.dpost_weight != nullptr) t.y = a.gate != nullptr ? s[2] * param(a.gate, mod) : s[2];
+  return t;
+}
+
+// Few groups (up to kFewGroups): one block does all groups of its channels, `slices` of its
+// 32 warps sharing each group, so one launch finishes everything.
+constexpr int kFewGroups = 128;
+__global__ void __launch_bounds__(1024) norm_bwd_finish_kernel(const __grid_constant__ FinalParams f) {
+  const BwdParams& p = f.b;
+  __shared__ float part[kSums][32][32];
+  __shared__ float2 terms[32][32];
+  const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * 32 + x;
+  const int at_once = 32 / f.slices, slice = y % f.slices, which = y / f.slices;
+  float2 total = make_float2(0.f, 0.f);
+  grid_dependency_wait();
+  for (uint32_t g0 = 0; g0 < f.groups; g0 += at_once) {
+    const uint32_t grp = g0 + which;
+    const bool mine = c < p.C && which < at_once && grp < f.groups;
+    float s[kSums] = {0.f, 0.f, 0.f};
+    if (mine) sum_runs(p, grp, c, slice, f.slices, s);
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) part[k][y][x] = s[k];
+    terms[y][x] = make_float2(0.f, 0.f);
+    __syncthreads();
+    if (mine && slice == 0) {
+      for (int o = 1; o < f.slices; ++o)
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) s[k] += part[k][y + o][x];
+      terms[y][x] = finish_group(p, grp, c, s);
+    }
+    __syncthreads();
+    if (y == 0)
+      for (int o = 0; o < at_once; ++o) {
+        total.x += terms[o * f.slices][x].x;
+        total.y += terms[o * f.slices][x].y;
+      }
+    __syncthreads();   // the next round clears the terms
   }
-  if (a.dpost_weight != nullptr) {
-    const float t = a.gate != nullptr ? s[2] * param(a.gate, mod) : s[2];
-    if (f.groups == 1) a.dpost_weight[c] = t; else base[2 * (int64_t)p.C] = t;
+  if (y == 0 && c < p.C) {
+    if (p.a.dweight != nullptr) p.a.dweight[c] = total.x;
+    if (p.a.dpost_weight != nullptr) p.a.dpost_weight[c] = total.y;
   }
 }
 
-// dweight and dpost_weight: the groups' terms in order, 32 threads per channel.
+// Many groups (of few runs each): a warp per group; the group's terms of dweight and
+// dpost_weight take its first run's place, and a second kernel adds them.
+constexpr int kGroupWarps = 8;
+__global__ void __launch_bounds__(32 * kGroupWarps) norm_bwd_groups_kernel(const __grid_constant__ FinalParams f) {
+  const BwdParams& p = f.b;
+  const int c = (blockIdx.x % f.channel_blocks) * 32 + threadIdx.x;
+  const int64_t grp = (int64_t)(blockIdx.x / f.channel_blocks) * kGroupWarps + threadIdx.y;
+  grid_dependency_wait();
+  if (c >= p.C || grp >= f.groups) return;
+  float s[kSums] = {0.f, 0.f, 0.f};
+  sum_runs(p, grp, c, 0, 1, s);
+  const float2 t = finish_group(p, grp, c, s);
+  float* base = p.partial + grp * p.chunks * kSums * p.C + c;
+  if (p.a.dweight != nullptr) base[p.C] = t.x;
+  if (p.a.dpost_weight != nullptr) base[2 * (int64_t)p.C] = t.y;
+}
+
 __global__ void __launch_bounds__(1024) norm_bwd_weights_kernel(const __grid_constant__ FinalParams f) {
   const BwdParams& p = f.b;
   __shared__ float part[32][33];
@@ -634,15 +667,16 @@ cudaError_t launch_norm_bwd(const NormGeom& g, const NormBwdArgs& a, void* works
   p.param_f32 = g.param_f32;
   f.groups = (uint32_t)g.groups;
   f.channel_blocks = (g.C + 31) / 32;
-  f.per_group = shape.chunks < kFinalY && g.groups > 1;
+  f.slices = g.groups < 32 ? 32 / (int)g.groups : 1;
   const int64_t items = g.groups * shape.chunks;
-  const int64_t group_blocks = (f.per_group ? (g.groups + kFinalY - 1) / kFinalY : g.groups) * f.channel_blocks;
+  const int64_t group_blocks = (g.groups + kGroupWarps - 1) / kGroupWarps * f.channel_blocks;
   if (items > INT32_MAX || group_blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t e = g.bf16 ? launch_type<__nv_bfloat16>(p, (unsigned)items, s) : launch_type<float>(p, (unsigned)items, s);
   if (e != cudaSuccess || p.need == 0) return e;
-  e = launch_dependent(norm_bwd_groups_kernel, dim3((unsigned)group_blocks), dim3(32, kFinalY), f, s);
-  if (e == cudaSuccess && g.groups > 1 && (a.dweight != nullptr || a.dpost_weight != nullptr))
-    e = launch_dependent(norm_bwd_weights_kernel, dim3((g.C + 31) / 32), dim3(32, 32), f, s);
+  if (g.groups <= kFewGroups) return launch_dependent(norm_bwd_finish_kernel, dim3(f.channel_blocks), dim3(32, 32), f, s);
+  e = launch_dependent(norm_bwd_groups_kernel, dim3((unsigned)group_blocks), dim3(32, kGroupWarps), f, s);
+  if (e == cudaSuccess && (a.dweight != nullptr || a.dpost_weight != nullptr))
+    e = launch_dependent(norm_bwd_weights_kernel, dim3(f.channel_blocks), dim3(32, 32), f, s);
   return e;
 }
 
