@@ -321,19 +321,20 @@ def ssta_forward(desc: Desc, q, k, v, q_text=None, k_text=None, v_text=None, str
         kp = ssta_tile_reorder(desc, k, k_text, stream=stream)
         vp = ssta_tile_reorder(desc, v, v_text, stream=stream)
         return _attend(desc, qp, kp, vp, stream, tile_scores)
-    with _on(stream, q.device):   # packed tensors dropped below go back to the stream that used them
-        packed, norms = [], []
-        for x, x_text, weight in ((q, q_text, q_weight), (k, k_text, k_weight), (v, v_text, None)):
-            p = ssta_tile_reorder(desc, x, x_text)
-            if weight is not None:
-                # pad rows are zeros and stay so
-                nd = norm_desc(p.numel() // desc.D, desc.D, desc.dtype, _VALUE_DTYPES[weight.dtype], "rms", eps=norm_eps)
-                y, _, rstd, kept = ssta_norm_fwd(nd, p, weight, y=p if checkpoint else None, save=checkpoint)
-                norms.append((nd, kept if checkpoint else p, rstd, weight))
-                p = y
-            elif x is not v:
-                norms.append(None)
-            packed.append(p)
+    for name, weight in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if weight is not None and weight.dtype not in _VALUE_DTYPES:
+            raise ValueError(f"{name} has dtype {weight.dtype}, expected torch.bfloat16 or torch.float32")
+    with _on(stream, _device(q, "q")):   # packed tensors dropped below go back to the stream that used them
+        packed = [ssta_tile_reorder(desc, *x) for x in ((q, q_text), (k, k_text), (v, v_text))]
+        norms = [None, None]
+        for i, weight in enumerate((q_weight, k_weight)):
+            if weight is None:
+                continue
+            # pad rows are zeros and stay so
+            p = packed[i]
+            nd = norm_desc(p.numel() // desc.D, desc.D, desc.dtype, _VALUE_DTYPES[weight.dtype], "rms", eps=norm_eps)
+            packed[i], _, rstd, kept = ssta_norm_fwd(nd, p, weight, y=p if checkpoint else None, save=checkpoint)
+            norms[i] = (nd, kept if checkpoint else p, rstd, weight)
         r = _attend(desc, *packed, None, tile_scores)
         r["saved"].norms = tuple(norms)
         if checkpoint is not None:
@@ -372,7 +373,7 @@ def ssta_backward(desc: Desc, saved: SstaSaved, dO, dO_text=None, stream=None):
     passes through the selection.  Returns a dict with dq, dk, dv (raster), dq_text, dk_text,
     dv_text (None without text), dq_weight, dk_weight ([D] float32, None without head norms)
     and the attention backward's workspace (ssta_read_device_status)."""
-    with _on(stream, dO.device):
+    with _on(stream, _device(dO, "dO")):
         do = ssta_tile_reorder(desc, dO, dO_text)
         rest = (saved.lse, do, saved.kv_idx, saved.kv_cnt)
         if isinstance(saved.q, Checkpoint):
@@ -391,6 +392,6 @@ def ssta_backward(desc: Desc, saved: SstaSaved, dO, dO_text=None, stream=None):
 
 
 from .norm import *  # noqa: E402,F401,F403  (needs the names above)
-from .norm import _VALUE_DTYPES, _on, __all__ as _norm_all  # noqa: E402
+from .norm import _VALUE_DTYPES, _device, _on, __all__ as _norm_all  # noqa: E402
 
 __all__ += _norm_all

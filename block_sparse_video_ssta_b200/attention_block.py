@@ -24,7 +24,7 @@ import torch
 
 from . import (Desc, SstaSaved, norm_desc, ssta_backward, ssta_checkpoint_load, ssta_forward, ssta_norm_bwd,
                ssta_norm_fwd, ssta_residual_norm_bwd, ssta_residual_norm_fwd, ssta_tile_unorder)
-from .norm import _VALUE_DTYPES, Checkpoint, _on
+from .norm import _VALUE_DTYPES, Checkpoint, _device, _on
 
 __all__ = ["BlockWeights", "BlockSaved", "BlockGrads", "ssta_block_forward", "ssta_block_backward"]
 
@@ -64,10 +64,13 @@ class BlockGrads:
     dk_norm: torch.Tensor | None
 
 
-def _check(desc, x, mod, w):
+def _check(desc, x, mod, w, **more):
+    """Shapes, dtypes and strides of the call's tensors (`more`: shaped like x); returns the norms' descriptor."""
     C, L = desc.H * desc.D, desc.T * desc.Y * desc.X + desc.L_text
-    for name, t, shape in (("x", x, (desc.B, L, C)), ("mod", mod, (desc.B, 5, C)), ("qkv", w.qkv, (3 * C, C)),
-                           ("out", w.out, (C, C))):
+    rows = [(name, t, (desc.B, L, C)) for name, t in (("x", x), *more.items())]
+    for name, t, shape in rows + [("mod", mod, (desc.B, 5, C)), ("qkv", w.qkv, (3 * C, C)), ("out", w.out, (C, C))]:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} is required")
         if tuple(t.shape) != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
         if not t.is_contiguous():
@@ -107,7 +110,7 @@ def ssta_block_forward(desc: Desc, x, mod, w: BlockWeights, checkpoint=None, str
     """Returns (r, n2 [B, L, C], saved).  ``checkpoint``: None (keep what the backward reads as it is), "int8" or
     "e4m3"."""
     nd = _check(desc, x, mod, w)
-    with _on(stream, x.device):
+    with _on(stream, _device(x, "x")):
         shift, scale, gate, shift2, scale2 = mod.unbind(1)
         n1, mean, rstd, x_saved = ssta_norm_fwd(nd, x, None, scale, shift, save=checkpoint)
         qkv = torch.matmul(n1, w.qkv.t()).view(desc.B, -1, 3, desc.H * desc.D)
@@ -124,8 +127,8 @@ def ssta_block_forward(desc: Desc, x, mod, w: BlockWeights, checkpoint=None, str
 def ssta_block_backward(desc: Desc, saved: BlockSaved, w: BlockWeights, dr, dn2, stream=None) -> BlockGrads:
     """Gradients from those of r and n2 [B, L, C]."""
     mod = saved.mod
-    nd = _check(desc, dr, mod, w)
-    with _on(stream, dr.device):
+    nd = _check(desc, dr, mod, w, dn2=dn2)
+    with _on(stream, _device(dr, "dr")):
         shift, scale, gate, _, scale2 = mod.unbind(1)
         g2 = ssta_residual_norm_bwd(nd, dr, dn2, saved.r, saved.y, saved.mean2, saved.rstd2, None, None, None, gate, None,
                                     scale2)

@@ -104,9 +104,11 @@ __device__ __forceinline__ V8 param8(const void* v, int64_t at, bool in, float o
 }
 
 // NV vectors per lane and row, U rows per thread, LPR lanes and WPR warps per row; POST:
-// with a gated residual.
+// with a gated residual.  Blocks per SM: four without a residual (64 registers; three and
+// 76 take 162 us instead of 152 us for 1,785,600 rows of 128 bf16 channels, and so do two
+// rows per thread with five blocks), three with one (80 registers), two where more is held.
 template <typename T, typename P, int NV, int U, int LPR, int WPR, bool POST>
-__global__ void __launch_bounds__(kFwdThreads, !POST ? 3 : sizeof(T) == 2 && WPR > 1 ? 3 : 2) norm_fwd_kernel(const __grid_constant__ FwdParams p) {
+__global__ void __launch_bounds__(kFwdThreads, !POST ? 4 : sizeof(T) == 2 && WPR > 1 ? 3 : 2) norm_fwd_kernel(const __grid_constant__ FwdParams p) {
   constexpr int kRowThreads = LPR * WPR, kSlots = kFwdThreads / kRowThreads;
   __shared__ float exchange[4 * U][kFwdThreads / 32];
   const int slot = threadIdx.x / kRowThreads, lane = threadIdx.x % kRowThreads;

@@ -108,6 +108,39 @@ def test_forward_and_backward_chain(cuda_ok, name, ov, normed, checkpoint):
             close(f"d{m}_weight", g[f"d{m}_weight"], t.grad, tol)
 
 
+def test_one_tensor_for_q_k_and_v(cuda_ok):
+    """The same tensor passed three times: its head norms and gradients stay apart."""
+    w = with_overrides(si.get_workload("tiny_f32"), T=3, Y=7, X=6)
+    d = S.desc_from(w)
+    x = si.make_inputs(w, 5, device="cuda")["q"]
+    weight = torch.linspace(0.5, 1.5, w.D, device="cuda")
+    for checkpoint in (None, "int8"):
+        a, b = (S.ssta_forward(d, x, y, z, q_weight=weight, checkpoint=checkpoint) for y, z in ((x, x), (x.clone(), x.clone())))
+        assert torch.equal(a["O"], b["O"])
+        ga, gb = (S.ssta_backward(d, r["saved"], x) for r in (a, b))
+        for n in ("dq", "dk", "dv", "dq_weight"):
+            assert torch.equal(ga[n], gb[n]), n
+        assert ga["dk_weight"] is None
+
+
+def test_chain_refusals(cuda_ok):
+    w = with_overrides(si.get_workload("tiny_f32"), L_text=5)
+    d = S.desc_from(w)
+    x = si.make_inputs(w, 0, device="cuda")
+    args = [x[n] for n in ("q", "k", "v", "q_text", "k_text", "v_text")]
+    weight = torch.ones(w.D, device="cuda")
+    for kw in (dict(q_weight=weight.half()), dict(q_weight=weight[:64]), dict(k_weight=weight.cpu()), dict(checkpoint="fp8")):
+        with pytest.raises(ValueError):
+            S.ssta_forward(d, *args, **kw)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        S.ssta_forward(d, *(t.cpu() for t in args), checkpoint="int8")
+    r = S.ssta_forward(d, *args, checkpoint="int8")
+    with pytest.raises(ValueError):
+        S.ssta_backward(d, r["saved"], x["q"])            # text gradient missing
+    with pytest.raises(ValueError):
+        S.ssta_backward(d, r["saved"], x["q"].bfloat16(), x["q_text"].bfloat16())
+
+
 def block_inputs(w, seed=0, normed=True):
     C, L = w.H * w.D, w.T * w.Y * w.X + w.L_text
     gen = torch.Generator().manual_seed(seed)
@@ -209,3 +242,6 @@ def test_block_refusals(cuda_ok):
     r, n2, saved = ssta_block_forward(d, x, mod, p, "int8")
     with pytest.raises(ValueError):
         ssta_block_backward(d, saved, p, dr[:, 1:], dn)
+    for a, b in ((dr, None), (None, dn), (dr, dn[:, 1:])):
+        with pytest.raises(ValueError):
+            ssta_block_backward(d, saved, p, a, b)
