@@ -412,6 +412,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     parity ^= 1;
   }
 
+  // the next kernel's blocks may take the SMs that run out of rows (they wait for the sums)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (p.need == 0) return;
   cp_wait<0>();
   if constexpr (NV == 1) {
@@ -451,14 +453,13 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   }
 }
 
-// The runs' sums, added in a fixed order, and every vector's gradient from them.  32
-// channels per block.  Launched as programmatic dependents of the kernel before: only their
-// launch overlaps it.
+// The runs' sums, added in a fixed order, and every vector's gradient from them.  Launched
+// as programmatic dependents of the kernel before: only their launch overlaps it.
 struct FinalParams {
   BwdParams b;
   uint32_t groups;
   int channel_blocks;
-  int slices;   // warps that share a group's runs
+  int slices;   // thread rows that share a group's runs
 };
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -491,44 +492,45 @@ __device__ __forceinline__ float2 finish_group(const BwdParams& p, int64_t grp, 
   return t;
 }
 
-// Few groups (up to kFewGroups): one block does all groups of its channels, `slices` of its
-// 32 warps sharing each group, so one launch finishes everything.
-constexpr int kFewGroups = 128;
-__global__ void __launch_bounds__(1024) norm_bwd_finish_kernel(const __grid_constant__ FinalParams f) {
+// Few groups (up to kFewGroups): one block does all groups of eight channels (one sector
+// per run and sum), `slices` of its 128 thread rows sharing each group, so one launch
+// finishes everything on as many SMs as there are sectors.
+constexpr int kFewGroups = 128, kFinishX = 8, kFinishY = 128;
+__global__ void __launch_bounds__(kFinishX * kFinishY) norm_bwd_finish_kernel(const __grid_constant__ FinalParams f) {
   const BwdParams& p = f.b;
-  __shared__ float part[kSums][32][32];
-  __shared__ float2 terms[32][32];
-  const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * 32 + x;
-  const int at_once = 32 / f.slices, slice = y % f.slices, which = y / f.slices;
-  float2 total = make_float2(0.f, 0.f);
+  __shared__ float part[kSums][kFinishY][kFinishX];
+  __shared__ float2 terms[kFinishY][kFinishX];
+  const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * kFinishX + x;   // C is a multiple of 8
+  const int slice = y % f.slices, grp = y / f.slices;
+  const bool mine = grp < f.groups;
   grid_dependency_wait();
-  for (uint32_t g0 = 0; g0 < f.groups; g0 += at_once) {
-    const uint32_t grp = g0 + which;
-    const bool mine = c < p.C && which < at_once && grp < f.groups;
-    float s[kSums] = {0.f, 0.f, 0.f};
-    if (mine) sum_runs(p, grp, c, slice, f.slices, s);
+  float s[kSums] = {0.f, 0.f, 0.f};
+  if (mine) sum_runs(p, grp, c, slice, f.slices, s);
+  // halve the slices of each group, then of all groups, in a fixed order
+  for (int n = f.slices; n > 1;) {
+    const int half = (n + 1) / 2;
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kSums; ++k) part[k][y][x] = s[k];
-    terms[y][x] = make_float2(0.f, 0.f);
     __syncthreads();
-    if (mine && slice == 0) {
-      for (int o = 1; o < f.slices; ++o)
+    if (slice + half < n) {
 #pragma unroll
-        for (int k = 0; k < kSums; ++k) s[k] += part[k][y + o][x];
-      terms[y][x] = finish_group(p, grp, c, s);
+      for (int k = 0; k < kSums; ++k) s[k] += part[k][y + half][x];
     }
-    __syncthreads();
-    if (y == 0)
-      for (int o = 0; o < at_once; ++o) {
-        total.x += terms[o * f.slices][x].x;
-        total.y += terms[o * f.slices][x].y;
-      }
-    __syncthreads();   // the next round clears the terms
+    n = half;
   }
-  if (y == 0 && c < p.C) {
-    if (p.a.dweight != nullptr) p.a.dweight[c] = total.x;
-    if (p.a.dpost_weight != nullptr) p.a.dpost_weight[c] = total.y;
+  float2 t = make_float2(0.f, 0.f);
+  if (mine && slice == 0) t = finish_group(p, grp, c, s);
+  if (p.a.dweight == nullptr && p.a.dpost_weight == nullptr) return;
+  if (slice == 0 && mine) terms[grp][x] = t;
+  __syncthreads();
+  if (y > 0) return;
+  for (int o = 1; o < (int)f.groups; ++o) {
+    t.x += terms[o][x].x;
+    t.y += terms[o][x].y;
   }
+  if (p.a.dweight != nullptr) p.a.dweight[c] = t.x;
+  if (p.a.dpost_weight != nullptr) p.a.dpost_weight[c] = t.y;
 }
 
 // Many groups (of few runs each): a warp per group; the group's terms of dweight and
@@ -667,13 +669,13 @@ cudaError_t launch_norm_bwd(const NormGeom& g, const NormBwdArgs& a, void* works
   p.param_f32 = g.param_f32;
   f.groups = (uint32_t)g.groups;
   f.channel_blocks = (g.C + 31) / 32;
-  f.slices = g.groups < 32 ? 32 / (int)g.groups : 1;
+  f.slices = g.groups < kFinishY ? kFinishY / (int)g.groups : 1;
   const int64_t items = g.groups * shape.chunks;
   const int64_t group_blocks = (g.groups + kGroupWarps - 1) / kGroupWarps * f.channel_blocks;
   if (items > INT32_MAX || group_blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t e = g.bf16 ? launch_type<__nv_bfloat16>(p, (unsigned)items, s) : launch_type<float>(p, (unsigned)items, s);
   if (e != cudaSuccess || p.need == 0) return e;
-  if (g.groups <= kFewGroups) return launch_dependent(norm_bwd_finish_kernel, dim3(f.channel_blocks), dim3(32, 32), f, s);
+  if (g.groups <= kFewGroups) return launch_dependent(norm_bwd_finish_kernel, dim3(g.C / kFinishX), dim3(kFinishX, kFinishY), f, s);
   e = launch_dependent(norm_bwd_groups_kernel, dim3((unsigned)group_blocks), dim3(32, kGroupWarps), f, s);
   if (e == cudaSuccess && (a.dweight != nullptr || a.dpost_weight != nullptr))
     e = launch_dependent(norm_bwd_weights_kernel, dim3(f.channel_blocks), dim3(32, 32), f, s);
