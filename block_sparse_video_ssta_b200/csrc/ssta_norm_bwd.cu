@@ -493,9 +493,9 @@ __device__ __forceinline__ float2 finish_group(const BwdParams& p, int64_t grp, 
 }
 
 // Few groups (up to kFewGroups): one block does all groups of eight channels (one sector
-// per run and sum), `slices` of its 128 thread rows sharing each group, so one launch
+// per run and sum), `slices` of its 64 thread rows sharing each group, so one launch
 // finishes everything on as many SMs as there are sectors.
-constexpr int kFewGroups = 128, kFinishX = 8, kFinishY = 128;
+constexpr int kFewGroups = 64, kFinishX = 8, kFinishY = 64;
 __global__ void __launch_bounds__(kFinishX * kFinishY) norm_bwd_finish_kernel(const __grid_constant__ FinalParams f) {
   const BwdParams& p = f.b;
   __shared__ float part[kSums][kFinishY][kFinishX];
