@@ -1,5 +1,5 @@
 /*
- * ssta.h — C ABI of the SSTA forward library (libssta.so) for NVIDIA B200 (sm_100a).
+ * ssta.h — C ABI of the SSTA library (libssta.so) for NVIDIA B200 (sm_100a).
  *
  * Selective and Sliding Tile Attention (SSTA) is the block-sparse self-attention
  * over the 3D (latent frame x height x width) token grid of a video diffusion
@@ -11,7 +11,9 @@
  *   Step 4  Combine masks + block-sparse attention -> ssta_build_block_mask (union,
  *                                                     compact lists) and
  *                                                     ssta_attention_fwd
- * plus ssta_tile_unorder, the inverse layout change of Step 1.
+ * plus ssta_tile_unorder, the inverse layout change of Step 1, ssta_attention_bwd, the
+ * gradients of Step 4, and the operators around the attention in a transformer block
+ * (norms, gated residuals, 8-bit activation checkpoints).
  *
  * Conventions shared by every call
  * --------------------------------
