@@ -1,4 +1,4 @@
-// Backward of Step 4 on the tensor cores, dQ part ("HunyuanVideo 1.5 Technical
+// Backward of Step 4 on the tensor cores (one grid for both parts, at the end); dQ part ("HunyuanVideo 1.5 Technical
 // Report", section "SSTA: Selective and Sliding Tile Attention", Step 4; the
 // attention equation softmax(Q K^T / sqrt(d_k)) V over the kept tiles):
 //   dQ = scale * dS K,  dS = P * (dO V^T - D),  P = exp(Q K^T * scale - LSE),
