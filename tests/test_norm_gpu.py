@@ -22,6 +22,12 @@ MODES = [("bf16", "f32", "layer", "none", True, 0, 1.0), ("bf16", "bf16", "rms",
 ALL = [s + m for i, s in enumerate(SIZES) for j, m in enumerate(MODES) if i % 3 == j % 3 or i in (1, 9, 12)]
 
 
+# rows beyond what the kernels for few rows take, in every width class of the others; the widest in fp32
+ALL += [s + m for s in [(1300, 512), (650, 520), (650, 768), (650, 776), (650, 1024), (350, 1032), (350, 1536), (350, 2048)]
+        for m in MODES[1:4]]
+ALL += [s + m for s in [(6, 6144), (5, 4104), (7, 8192)] for m in MODES[2:4]]
+
+
 def make(rows, C, dtype, param, norm, post, vectors, mod_rows, res_scale, **kw):
     return Case(rows, C, dtype, param, norm, post, vectors, mod_rows, res_scale, **kw)
 
@@ -167,6 +173,116 @@ def test_residual_norm_matches_oracle(cuda_ok, cfg):
             assert torch.equal(saved.exponents, alone.exponents)
         rv, yv = S.ssta_checkpoint_load(s.saved_r), S.ssta_checkpoint_load(s.saved_y)
         check_residual_bwd(c, s, s.saved_r, s.saved_y, rv, yv)
+
+
+VECTORS = ("weight", "scale", "shift", "gate", "post_weight")
+
+
+@pytest.mark.parametrize("given", [(), ("scale",), ("shift",), ("weight",), ("gate",), ("post_weight",), ("weight", "shift"),
+                                   ("scale", "gate")], ids=str)
+@pytest.mark.parametrize("rows,C", [(9, 264), (1300, 512)])
+def test_each_vector_alone(cuda_ok, rows, C, given):
+    """Any subset of the vectors; gradients of the absent ones (as 1 or 0) are there for the asking."""
+    c = make(rows, C, "bf16", "f32", "layer", "rms", True, rows // 2 + 1, 1.0)
+    for v in VECTORS:
+        if v not in given:
+            setattr(c, v, None)
+    mean, rstd = check_norm_fwd(c)
+    check_norm_bwd(c, mean, rstd, c.x, c.x)
+    f = check_residual_fwd(c)
+    check_residual_bwd(c, f, f.r, c.y, f.r, c.y)
+    # by default only the given vectors' gradients are computed
+    g = S.ssta_residual_norm_bwd(c.desc, c.dr, c.dn, f.r, c.y, f.mean, f.rstd, f.post_mean, f.post_rstd, c.post_weight, c.gate,
+                                 c.weight, c.scale)
+    for v in VECTORS:
+        assert (getattr(g, "d" + v) is not None) == (getattr(c, "scale" if v == "shift" else v) is not None), v
+
+
+def test_optional_outputs_do_not_change_the_others(cuda_ok):
+    c = make(100, 1000, "bf16", "f32", "rms", "none", True, 30, 1.0)
+    _, _, rstd, _ = S.ssta_norm_fwd(c.desc, c.x)
+    full = S.ssta_norm_bwd(c.desc, c.dn, c.x, None, rstd, c.weight, c.scale, c.dr)
+    none = S.ssta_norm_bwd(c.desc, c.dn, c.x, None, rstd, c.weight, c.scale, c.dr, want_dshift=False)
+    assert none.dshift is None and torch.equal(none.dx, full.dx) and torch.equal(none.dscale, full.dscale)
+    bare = S.ssta_norm_bwd(c.desc, c.dn, c.x, None, rstd)
+    assert bare.dweight is None and bare.dscale is None and bare.dshift is None
+    zero = S.ssta_norm_bwd(c.desc, c.dn, c.x, None, rstd, dres=torch.zeros_like(c.dr))
+    assert torch.equal(bare.dx, zero.dx)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tensors_at_16_byte_offsets(cuda_ok, dtype):
+    """16 bytes is all the alignment a tensor needs, also where 32-byte accesses are used otherwise."""
+    c = make(300, 520, dtype, dtype, "layer", "rms", True, 77, 1.0)
+    item = c.x.element_size()
+
+    def shift(t):
+        if t is None:
+            return None
+        buf = torch.empty(t.numel() * t.element_size() + 64, dtype=torch.uint8, device="cuda")
+        base = 16 if buf.data_ptr() % 32 == 0 else 0
+        out = buf[base:base + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        assert out.data_ptr() % 32 == 16
+        return out.copy_(t)
+
+    wide = {n: getattr(c, n).contiguous() for n in ("scale", "shift", "gate")}
+    d = S.norm_desc(c.rows, c.C, dtype, dtype, "layer", "rms", c.eps, 1.0, c.mod_rows)
+    plain = dict(x=c.x, y=c.y, post_weight=c.post_weight, weight=c.weight, **wide)
+    back = dict(dr=c.dr, dn=c.dn)
+
+    def go(t, b, out):
+        f = S.ssta_residual_norm_fwd(d, t["x"], t["y"], t["post_weight"], t["gate"], t["weight"], t["scale"], t["shift"],
+                                     r=out(torch.empty_like(c.x)), n=out(torch.empty_like(c.x)), save_y="int8")
+        g = S.ssta_residual_norm_bwd(d, b["dr"], b["dn"], f.r, t["y"], f.mean, f.rstd, f.post_mean, f.post_rstd,
+                                     t["post_weight"], t["gate"], t["weight"], t["scale"], dx=out(torch.empty_like(c.x)),
+                                     dy=out(torch.empty_like(c.x)))
+        ck = S.ssta_checkpoint_save(f.r, "e4m3")
+        v = S.ssta_checkpoint_load(ck, out(torch.empty_like(c.x)))
+        return [f.r, f.n, f.mean, f.saved_y.codes, g.dx, g.dy, g.dgate, g.dscale, g.dshift, g.dweight, g.dpost_weight, v]
+
+    a = go(plain, back, lambda t: t)
+    b = go({n: shift(t) for n, t in plain.items()}, {n: shift(t) for n, t in back.items()}, shift)
+    for i, (p, q) in enumerate(zip(a, b)):
+        assert torch.equal(p, q), i
+    with pytest.raises(S.SstaError) as e:
+        S.ssta_norm_fwd(d, torch.empty(c.rows * c.C + 8, dtype=c.x.dtype, device="cuda")[8 // item:][:c.rows * c.C].view(c.rows, c.C))
+    assert e.value.code == 3
+
+
+@pytest.mark.parametrize("dtype,C,saved", [("bf16", 264, None), ("bf16", 128, "int8"), ("f32", 136, "e4m3"), ("f32", 128, None),
+                                           ("bf16", 2048, "e4m3")])
+def test_long_runs(cuda_ok, dtype, C, saved):
+    """Many rows per block (its row table is refilled, its stages wrap, groups end inside tiles), every element
+    against float64 autograd on the GPU.  Bounds as relative 2-norms: half a step of the type for the rows, and for the
+    vectors' sums over n rows sqrt(n) u * 4, the square-root growth of rounding in a sum of independent terms."""
+    rows = 70_001 if C < 1024 else 40_003
+    c = make(rows, C, dtype, "f32", "layer", "rms", True, rows // 2 - 77, 0.5, offset=0.1)
+    f = S.ssta_residual_norm_fwd(c.desc, c.x, c.y, c.post_weight, c.gate, c.weight, c.scale, c.shift, save_y=saved, save_r=saved)
+    r, y = (f.saved_r, f.saved_y) if saved else (f.r, c.y)
+    g = S.ssta_residual_norm_bwd(c.desc, c.dr, c.dn, r, y, f.mean, f.rstd, f.post_mean, f.post_rstd, c.post_weight, c.gate,
+                                 c.weight, c.scale)
+    value = lambda t: (S.ssta_checkpoint_load(t) if saved else t).double()
+    group = torch.arange(rows, device="cuda") // (rows // 2 - 77)
+    v = {n: getattr(c, n).double().requires_grad_() for n in VECTORS}
+    rows_of = lambda n: v[n].index_select(0, group)
+    # the norms' gradients at the saved statistics: through(x) = the norm's exact derivative with fixed mean and rstd
+    rh = (value(r) - f.mean.double()[:, None]) * f.rstd.double()[:, None]
+    yh = value(y) * f.post_rstd.double()[:, None]
+
+    def through(h, grad, rstd, layer):
+        out = grad - h * (grad * h).mean(1, keepdim=True) - (grad.mean(1, keepdim=True) if layer else 0)
+        return out * rstd.double()[:, None]
+
+    gr = c.dn.double() * v["weight"] * (1 + rows_of("scale"))
+    dR = c.dr.double() + through(rh, gr.detach(), f.rstd, True)
+    loss = (c.dn.double() * (rh * v["weight"] * (1 + rows_of("scale")) + rows_of("shift"))).sum() + \
+        (dR * rows_of("gate") * yh * v["post_weight"]).sum()
+    loss.backward()
+    dh = dR * rows_of("gate").detach() * v["post_weight"].detach()
+    rel = lambda a, b: ((a.double() - b).norm() / b.norm()).item()
+    assert rel(g.dx, 0.5 * dR) <= c.half and rel(g.dy, through(yh, dh, f.post_rstd, False)) <= c.half + 4 * U
+    for n in VECTORS:
+        assert rel(getattr(g, "d" + n), v[n].grad) <= 4 * U * rows ** 0.5, n
 
 
 def test_fused_save_of_the_norm_input(cuda_ok):
