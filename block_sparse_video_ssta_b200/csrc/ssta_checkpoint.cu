@@ -1,7 +1,8 @@
 // 8-bit activation checkpoints on their own: save (quantise) and load (values back).
 // Elementwise over groups of 128 channels, one half-warp per group (8 channels per lane:
 // a group's largest magnitude is three register steps and four shuffles), bound by HBM:
-// 3 bytes per bf16 element and 1/128 byte of exponents in either direction.
+// 3 bytes per bf16 element and 1/128 byte of exponents in either direction.  219,600 x
+// 2,048 bf16 there and back: 400 us, 6.8 TB/s, 1.03 of the measured copy rate.
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
 

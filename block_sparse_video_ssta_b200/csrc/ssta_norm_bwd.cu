@@ -10,17 +10,20 @@
 // A block walks a run of rows of one group, so a thread keeps the same eight channels
 // throughout: its share of S1-S3 and the products of the vectors stay in registers, and
 // the sums leave the SM once per run instead of once per row.  The rows ahead come by
-// cp.async into slots of shared memory that only the copying thread reads: several rows
-// are in flight per thread without registers and without a barrier (channels and rows
-// that do not exist are filled with zeros there, so the arithmetic has no conditions).
+// cp.async into slots of shared memory that only the copying thread (fp32: its warp)
+// reads: several rows are in flight per thread without registers and without a block-wide
+// barrier (channels and rows that do not exist are filled with zeros there, so the
+// arithmetic has no conditions).
 // r and y may be 8-bit checkpoints: their codes are what is copied, and they are decoded
 // on the way to registers, which saves one of the two bytes of a bf16 read.  A small
 // kernel adds the runs' sums in a fixed order (no atomics: equal inputs give equal bytes).
 //
-// What bounds it: HBM, once the instructions fit.  A thread handles two rows at a time
-// (bf16) and works on pairs of channels; the row sums of both rows share one butterfly,
-// in which a lane gives away the sums that it need not finish (6 shuffles for four sums
-// instead of 20).
+// What bounds it: HBM, once the instructions fit.  A thread handles two rows at a time and
+// works on pairs of channels; the row sums of both rows share one butterfly, in which a
+// lane gives away the sums that it need not finish (6 shuffles for four sums instead of
+// 20).  219,600 x 2,048 bf16 (gradients of r and n in, of x and y out): 725 us from int8
+// checkpoints, 6.2 TB/s, 0.95 of the measured copy rate; 920 us dense (0.89).  One row at a
+// time in scalar arithmetic took 1,165 and 986 us.
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
 
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   };
   // Fills the table for the kWindow rows from w0 on (rstd and group scales 0 where there is
   // no row).  The first kWindow threads fetch the rows' scalars, the others the exponents.
-  static_assert(kWindow == 64, "blocks have at least 160 threads");
+  static_assert(kWindow < 160, "a block has at least 160 threads");
   auto fill_table = [&](int w0) {
     if (w0 > 0) __syncthreads();
     if (threadIdx.x < kWindow) {
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(kFinishX * kFinishY) norm_bwd_finish_kernel(co
 #pragma unroll
     for (int k = 0; k < kSums; ++k) part[k][y][x] = s[k];
     __syncthreads();
-    if (slice + half < n) {
+    if (mine && slice + half < n) {
 #pragma unroll
       for (int k = 0; k < kSums; ++k) s[k] += part[k][y + half][x];
     }

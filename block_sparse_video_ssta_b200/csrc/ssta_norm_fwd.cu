@@ -9,6 +9,8 @@
 // a thread holds four vectors of 8 channels per array, of one wide row or of several
 // narrow ones, which keeps enough loads in flight without any staging.  Weights and modulation rows are shared by many rows and come from L1/L2.
 // An 8-bit checkpoint of an input or of r is written in the same pass from the registers.
+// Measured, of the measured copy rate: residual and norm of 111,600 x 2,048 bf16 295 us
+// (0.94), RMS norm of 1,785,600 x 128 bf16 152 us (0.93), 97,656 x 1,024 fp32 0.98.
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
 

@@ -107,7 +107,7 @@ class Checkpoint:
     """An activation kept in 8 bits: ``codes`` [..., C] (torch.int8 or torch.float8_e4m3fn), ``exponents``
     [..., ceil(C / 128)] (torch.uint8), and the ``dtype`` its values are read as.  The value of a code is
     code * 2^(exponent - 127); exponent 255 marks a group that held an infinity or a NaN (its values read as NaN)."""
-    __slots__ = ("codes", "exponents", "dtype", "_c")
+    __slots__ = ("_codes", "_exponents", "_dtype")
 
     def __init__(self, codes, exponents, dtype=torch.bfloat16):
         if codes.dtype not in _CODE_NAMES:
@@ -121,27 +121,27 @@ class Checkpoint:
         _ptr(exponents, "exponents", torch.uint8, want)
         if exponents.device != codes.device:
             raise ValueError(f"exponents are on {exponents.device}, codes on {codes.device}")
-        self._set(codes, exponents, dtype)
+        self._codes, self._exponents, self._dtype = codes, exponents, dtype
 
-    def _set(self, codes, exponents, dtype):
-        self.codes, self.exponents, self.dtype = codes, exponents, dtype
-        self._c = _Ckpt(codes.data_ptr(), exponents.data_ptr(), FORMATS[_CODE_NAMES[codes.dtype]])
+    codes = property(lambda self: self._codes)
+    exponents = property(lambda self: self._exponents)
+    dtype = property(lambda self: self._dtype)
 
     @property
     def format(self) -> str:
-        return _CODE_NAMES[self.codes.dtype]
+        return _CODE_NAMES[self._codes.dtype]
 
     @property
     def shape(self):
-        return self.codes.shape
+        return self._codes.shape
 
     @property
     def device(self):
-        return self.codes.device
+        return self._codes.device
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.exponents.numel()
+        return self._codes.numel() + self._exponents.numel()
 
     @classmethod
     def empty(cls, shape, format="int8", dtype=torch.bfloat16, device="cuda") -> "Checkpoint":
@@ -152,9 +152,14 @@ class Checkpoint:
             raise ValueError(f"values have dtype {dtype}, expected torch.bfloat16 or torch.float32")
         shape = tuple(shape)
         ckpt = cls.__new__(cls)
-        ckpt._set(torch.empty(shape, dtype=_CODE_DTYPES[format], device=device),
-                  torch.empty(shape[:-1] + (-(-shape[-1] // GROUP),), dtype=torch.uint8, device=device), dtype)
+        ckpt._codes = torch.empty(shape, dtype=_CODE_DTYPES[format], device=device)
+        ckpt._exponents = torch.empty(shape[:-1] + (-(-shape[-1] // GROUP),), dtype=torch.uint8, device=device)
+        ckpt._dtype = dtype
         return ckpt
+
+    def _ref(self):
+        """The C struct of this moment's addresses, by reference."""
+        return ctypes.byref(_Ckpt(self._codes.data_ptr(), self._exponents.data_ptr(), FORMATS[self.format]))
 
 
 @dataclass
@@ -292,7 +297,7 @@ class _Args:
             raise ValueError(f"{name} must be a checkpoint on {self.dev}")
         if t.codes.numel() != self.n or t.shape[-1] != self.C:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.rows} rows of {self.C}")
-        return None, ctypes.byref(t._c)
+        return None, t._ref()
 
     def save(self, want, like, name):
         """The checkpoint to write: a new one of a named format, or the caller's."""
@@ -323,7 +328,7 @@ class _Args:
 
 
 def _ref(ckpt):
-    return None if ckpt is None else ctypes.byref(ckpt._c)
+    return None if ckpt is None else ckpt._ref()
 
 
 def ssta_norm_fwd(desc: NormDesc, x, weight=None, scale=None, shift=None, y=None, mean=None, rstd=None, save=None,
@@ -443,7 +448,7 @@ def ssta_checkpoint_save(x, format="int8", out=None, stream=None) -> Checkpoint:
             raise ValueError(f"out must be a Checkpoint of shape {tuple(x.shape)} and dtype {x.dtype} on {dev}")
         C = x.shape[-1]
         _check(lib.ssta_checkpoint_save(x.numel() // max(C, 1), C, _VALUE_DTYPES[x.dtype], _ptr(x, "x"),
-                                        ctypes.byref(out._c), _current(dev)), "ssta_checkpoint_save")
+                                        out._ref(), _current(dev)), "ssta_checkpoint_save")
     return out
 
 
@@ -458,7 +463,7 @@ def ssta_checkpoint_load(ckpt: Checkpoint, x=None, stream=None):
         elif x.device != dev:
             raise ValueError(f"x must be a tensor on {dev}")
         C = ckpt.shape[-1]
-        _check(lib.ssta_checkpoint_load(x.numel() // max(C, 1), C, _VALUE_DTYPES[ckpt.dtype], ctypes.byref(ckpt._c),
+        _check(lib.ssta_checkpoint_load(x.numel() // max(C, 1), C, _VALUE_DTYPES[ckpt.dtype], ckpt._ref(),
                                         _ptr(x, "x", ckpt.dtype, ckpt.shape), _current(dev)), "ssta_checkpoint_load")
     return x
 

@@ -99,6 +99,20 @@ def test_buffers_are_reused_and_framed(cuda_ok):
         assert (out[0] == 5).all() and (out[10] == 5).all()
 
 
+def test_addresses_are_those_of_the_call(cuda_ok):
+    """A checkpoint's tensors cannot be swapped for others, and where their storage moves the call follows."""
+    x = torch.randn(16, 256, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    ck = S.ssta_checkpoint_save(x)
+    want = S.ssta_checkpoint_load(ck)
+    with pytest.raises(AttributeError):
+        ck.codes = ck.codes.clone()
+    old = ck.codes.clone()
+    keep = ck.codes.data
+    ck.codes.data = old.clone()       # the same values elsewhere
+    keep.zero_()
+    assert torch.equal(S.ssta_checkpoint_load(ck), want)
+
+
 # The kernels behind are those of ssta_attention_bwd; the tolerances are those of its test, for the same arithmetic.
 TOL = {"f32": dict(rel=1e-4, mx=1e-4, row=1e-4), "bf16": dict(rel=1e-2, mx=2e-2, row=5e-2)}
 ATTENTION = [
