@@ -157,6 +157,17 @@ class Checkpoint:
         ckpt._dtype = dtype
         return ckpt
 
+    @classmethod
+    def _like(cls, t, format, dtype) -> "Checkpoint":
+        """An unwritten checkpoint of a contiguous tensor (or of one shaped like it)."""
+        if format not in _CODE_DTYPES:
+            raise ValueError(f"format {format!r}, expected one of {sorted(_CODE_DTYPES)}")
+        ckpt = cls.__new__(cls)
+        ckpt._codes = torch.empty_like(t, dtype=_CODE_DTYPES[format])
+        ckpt._exponents = t.new_empty(t.shape[:-1] + (-(-t.shape[-1] // GROUP),), dtype=torch.uint8)
+        ckpt._dtype = dtype
+        return ckpt
+
     def _ref(self):
         """The C struct of this moment's addresses, by reference."""
         return ctypes.byref(_Ckpt(self._codes.data_ptr(), self._exponents.data_ptr(), FORMATS[self.format]))
@@ -304,7 +315,7 @@ class _Args:
         if want is None:
             return None
         if isinstance(want, str):
-            return Checkpoint.empty(like.shape, want, self.dtype, self.dev)
+            return Checkpoint._like(like, want, self.dtype)
         if not isinstance(want, Checkpoint):
             raise ValueError(f"{name} must be a format name or a Checkpoint")
         self.kept(want, name)
@@ -312,18 +323,37 @@ class _Args:
             raise ValueError(f"{name} holds values of dtype {want.dtype}, expected {self.dtype}")
         return want
 
-    def new_act(self, t, like):
-        """An output shaped like a checked activation."""
-        return torch.empty_like(like) if t is None else t
+    # Outputs: (tensor, address) of the caller's tensor, checked, or of a new one.
 
-    def new_f32(self, t, *shape, like=None):
-        if t is not None:
-            return t
-        return torch.empty(shape, dtype=torch.float32, device=self.dev) if like is None else torch.empty_like(like)
+    def out_act(self, t, name, like):
+        """Shaped like a checked activation."""
+        if t is None:
+            t = torch.empty_like(like)
+            return t, t.data_ptr()
+        return t, self.act(t, name)
+
+    def out_stat(self, t, name, wanted, like=None):
+        if t is None:
+            if not wanted:
+                return None, None
+            t = torch.empty_like(like) if like is not None else torch.empty(self.rows, dtype=torch.float32, device=self.dev)
+            return t, t.data_ptr()
+        return t, self.stat(t, name)
+
+    def out_grad(self, t, name, wanted, groups=None, like=None):
+        """[C], or [groups, C]."""
+        if t is None:
+            if not wanted:
+                return None, None
+            shape = (self.C,) if groups is None else (groups, self.C)
+            t = torch.empty_like(like) if like is not None else torch.empty(shape, dtype=torch.float32, device=self.dev)
+            return t, t.data_ptr()
+        return t, self.grad(t, name, groups or 1)
 
     def workspace(self, t):
         if t is None:
             t = _workspace(_bwd_bytes(self.rows, self.C, self.desc.mod_rows), self.dev)
+            return t, t.data_ptr()
         return t, self._dense(t, "workspace", torch.uint8, t.numel(), 0)
 
 
@@ -341,14 +371,13 @@ def ssta_norm_fwd(desc: NormDesc, x, weight=None, scale=None, shift=None, y=None
     with _on(stream, dev):
         a = _Args(desc, dev)
         px = a.act(x, "x")
-        y = a.new_act(y, x)
-        if stats:
-            mean = a.new_f32(mean, a.rows) if desc.norm == 1 else mean
-            rstd = a.new_f32(rstd, a.rows, like=mean)
+        y, py = a.out_act(y, "y", x)
+        mean, pm = a.out_stat(mean, "mean", stats and desc.norm == 1)
+        rstd, pr = a.out_stat(rstd, "rstd", stats, mean)
         saved = a.save(save, x, "save")
         _check(lib.ssta_norm_fwd(
             ctypes.byref(desc), px, a.weight(weight, "weight"), a.mod(scale, "scale"), a.mod(shift, "shift"),
-            a.act(y, "y"), a.stat(mean, "mean"), a.stat(rstd, "rstd"), _ref(saved), _current(dev)), "ssta_norm_fwd")
+            py, pm, pr, _ref(saved), _current(dev)), "ssta_norm_fwd")
     return y, mean, rstd, saved
 
 
@@ -362,17 +391,15 @@ def ssta_norm_bwd(desc: NormDesc, dy, x, mean, rstd, weight=None, scale=None, dr
         a = _Args(desc, dev)
         pdy = a.act(dy, "dy")
         px, cx = a.kept(x, "x")
-        dx = a.new_act(dx, dy)
-        dweight = a.new_f32(dweight, a.C) if weight is not None else dweight
-        dscale = a.new_f32(dscale, a.groups, a.C) if scale is not None else dscale
-        if want_dshift if want_dshift is not None else scale is not None:
-            dshift = a.new_f32(dshift, a.groups, a.C, like=dscale)
+        dx, pdx = a.out_act(dx, "dx", dy)
+        dweight, pdw = a.out_grad(dweight, "dweight", weight is not None)
+        dscale, pds = a.out_grad(dscale, "dscale", scale is not None, a.groups)
+        dshift, pdt = a.out_grad(dshift, "dshift", scale is not None if want_dshift is None else want_dshift, a.groups, dscale)
         workspace, pw = a.workspace(workspace)
         _check(lib.ssta_norm_bwd(
             ctypes.byref(desc), pdy, px, cx, a.stat(mean, "mean"), a.stat(rstd, "rstd"), a.weight(weight, "weight"),
-            a.mod(scale, "scale"), a.act(dres, "dres"), a.act(dx, "dx"), a.grad(dweight, "dweight", 1),
-            a.grad(dscale, "dscale", a.groups), a.grad(dshift, "dshift", a.groups), pw, workspace.numel(),
-            _current(dev)), "ssta_norm_bwd")
+            a.mod(scale, "scale"), a.act(dres, "dres"), pdx, pdw, pds, pdt, pw, workspace.numel(), _current(dev)),
+            "ssta_norm_bwd")
     return NormGrads(dx, dweight, dscale, dshift, workspace)
 
 
@@ -386,19 +413,17 @@ def ssta_residual_norm_fwd(desc: NormDesc, x, y, post_weight=None, gate=None, we
     with _on(stream, dev):
         a = _Args(desc, dev)
         px, py = a.act(x, "x"), a.act(y, "y")
-        r = a.new_act(r, x)
-        n = a.new_act(n, x) if desc.norm != 0 else n
-        stat = lambda on, like=None: a.new_f32(None, a.rows, like=like) if stats and on else None
-        pr = stat(desc.post_norm != 0)
-        pm = stat(desc.post_norm == 1, pr)
-        rs = stat(desc.norm != 0, pr)
-        m = stat(desc.norm == 1, rs)
+        r, p_r = a.out_act(r, "r", x)
+        n, p_n = a.out_act(n, "n", x) if desc.norm != 0 or n is not None else (None, None)
+        pr, p_pr = a.out_stat(None, "post_rstd", stats and desc.post_norm != 0)
+        pm, p_pm = a.out_stat(None, "post_mean", stats and desc.post_norm == 1, pr)
+        rs, p_rs = a.out_stat(None, "rstd", stats and desc.norm != 0, pr)
+        m, p_m = a.out_stat(None, "mean", stats and desc.norm == 1, rs)
         cy, cr = a.save(save_y, y, "save_y"), a.save(save_r, x, "save_r")
         _check(lib.ssta_residual_norm_fwd(
             ctypes.byref(desc), px, py, a.weight(post_weight, "post_weight"), a.mod(gate, "gate"),
-            a.weight(weight, "weight"), a.mod(scale, "scale"), a.mod(shift, "shift"), a.act(r, "r"), a.act(n, "n"),
-            a.stat(pm, "post_mean"), a.stat(pr, "post_rstd"), a.stat(m, "mean"), a.stat(rs, "rstd"), _ref(cy), _ref(cr),
-            _current(dev)), "ssta_residual_norm_fwd")
+            a.weight(weight, "weight"), a.mod(scale, "scale"), a.mod(shift, "shift"), p_r, p_n, p_pm, p_pr, p_m, p_rs,
+            _ref(cy), _ref(cr), _current(dev)), "ssta_residual_norm_fwd")
     return ResidualNorm(r, n, pm, pr, m, rs, cy, cr)
 
 
@@ -415,40 +440,41 @@ def ssta_residual_norm_bwd(desc: NormDesc, dr, dn, r=None, y=None, mean=None, rs
     with _on(stream, dev):
         a = _Args(desc, dev)
         (pr_, cr), (py, cy) = a.kept(r, "r"), a.kept(y, "y")
-        dx, dy = a.new_act(dx, like), a.new_act(dy, like)
-        dpost_weight = a.new_f32(dpost_weight, a.C) if post_weight is not None else dpost_weight
-        dgate = a.new_f32(dgate, a.groups, a.C) if gate is not None else dgate
-        if dn is not None:
-            dweight = a.new_f32(dweight, a.C) if weight is not None else dweight
-            dscale = a.new_f32(dscale, a.groups, a.C) if scale is not None else dscale
-            if want_dshift if want_dshift is not None else scale is not None:
-                dshift = a.new_f32(dshift, a.groups, a.C, like=dscale)
+        pdr, pdn = a.act(dr, "dr"), a.act(dn, "dn")
+        dx, pdx = a.out_act(dx, "dx", like)
+        dy, pdy = a.out_act(dy, "dy", like)
+        normed = dn is not None
+        dpost_weight, pdp = a.out_grad(dpost_weight, "dpost_weight", post_weight is not None)
+        dgate, pdg = a.out_grad(dgate, "dgate", gate is not None, a.groups)
+        dweight, pdw = a.out_grad(dweight, "dweight", normed and weight is not None)
+        dscale, pds = a.out_grad(dscale, "dscale", normed and scale is not None, a.groups, dgate)
+        dshift, pdt = a.out_grad(dshift, "dshift", normed and (scale is not None if want_dshift is None else want_dshift),
+                                 a.groups, dscale)
         workspace, pw = a.workspace(workspace)
         _check(lib.ssta_residual_norm_bwd(
-            ctypes.byref(desc), a.act(dr, "dr"), a.act(dn, "dn"), pr_, cr, py, cy, a.stat(post_mean, "post_mean"),
-            a.stat(post_rstd, "post_rstd"), a.stat(mean, "mean"), a.stat(rstd, "rstd"),
-            a.weight(post_weight, "post_weight"), a.mod(gate, "gate"), a.weight(weight, "weight"), a.mod(scale, "scale"),
-            a.act(dx, "dx"), a.act(dy, "dy"), a.grad(dpost_weight, "dpost_weight", 1), a.grad(dgate, "dgate", a.groups),
-            a.grad(dweight, "dweight", 1), a.grad(dscale, "dscale", a.groups), a.grad(dshift, "dshift", a.groups), pw,
-            workspace.numel(), _current(dev)), "ssta_residual_norm_bwd")
+            ctypes.byref(desc), pdr, pdn, pr_, cr, py, cy, a.stat(post_mean, "post_mean"), a.stat(post_rstd, "post_rstd"),
+            a.stat(mean, "mean"), a.stat(rstd, "rstd"), a.weight(post_weight, "post_weight"), a.mod(gate, "gate"),
+            a.weight(weight, "weight"), a.mod(scale, "scale"), pdx, pdy, pdp, pdg, pdw, pds, pdt, pw, workspace.numel(),
+            _current(dev)), "ssta_residual_norm_bwd")
     return ResidualNormGrads(dx, dy, dpost_weight, dgate, dweight, dscale, dshift, workspace)
 
 
 def ssta_checkpoint_save(x, format="int8", out=None, stream=None) -> Checkpoint:
     """The 8-bit checkpoint of x [..., C] (bf16 or f32), in ``out`` or a new one of ``format``."""
     dev = _device(x, "x")
+    if x.dtype not in _VALUE_DTYPES:
+        raise ValueError(f"x has dtype {x.dtype}, expected torch.bfloat16 or torch.float32")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
     with _on(stream, dev):
-        if x.dtype not in _VALUE_DTYPES:
-            raise ValueError(f"x has dtype {x.dtype}, expected torch.bfloat16 or torch.float32")
-        if x.dim() < 1:
-            raise ValueError("x must have at least one dimension")
+        px = _ptr(x, "x")
         if out is None:
-            out = Checkpoint.empty(x.shape, format, x.dtype, dev)
+            out = Checkpoint._like(x, format, x.dtype)
         elif not isinstance(out, Checkpoint) or out.device != dev or out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError(f"out must be a Checkpoint of shape {tuple(x.shape)} and dtype {x.dtype} on {dev}")
         C = x.shape[-1]
-        _check(lib.ssta_checkpoint_save(x.numel() // max(C, 1), C, _VALUE_DTYPES[x.dtype], _ptr(x, "x"),
-                                        out._ref(), _current(dev)), "ssta_checkpoint_save")
+        _check(lib.ssta_checkpoint_save(x.numel() // max(C, 1), C, _VALUE_DTYPES[x.dtype], px, out._ref(), _current(dev)),
+               "ssta_checkpoint_save")
     return out
 
 
@@ -459,12 +485,15 @@ def ssta_checkpoint_load(ckpt: Checkpoint, x=None, stream=None):
         raise ValueError("ckpt must be a Checkpoint")
     with _on(stream, dev):
         if x is None:
-            x = torch.empty(ckpt.shape, dtype=ckpt.dtype, device=dev)
-        elif x.device != dev:
-            raise ValueError(f"x must be a tensor on {dev}")
-        C = ckpt.shape[-1]
-        _check(lib.ssta_checkpoint_load(x.numel() // max(C, 1), C, _VALUE_DTYPES[ckpt.dtype], ckpt._ref(),
-                                        _ptr(x, "x", ckpt.dtype, ckpt.shape), _current(dev)), "ssta_checkpoint_load")
+            x = torch.empty_like(ckpt._codes, dtype=ckpt._dtype)
+            px = x.data_ptr()
+        else:
+            px = _ptr(x, "x", ckpt.dtype, ckpt.shape)
+            if x.device != dev:
+                raise ValueError(f"x must be a tensor on {dev}")
+        C = x.shape[-1]
+        _check(lib.ssta_checkpoint_load(x.numel() // max(C, 1), C, _VALUE_DTYPES[ckpt._dtype], ckpt._ref(), px,
+                                        _current(dev)), "ssta_checkpoint_load")
     return x
 
 
