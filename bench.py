@@ -628,7 +628,7 @@ def run_backward(args):
         "roofline": {"bound": "tensor", "achieved": tflops, "peak": peak, "unit": "TFLOP/s", "frac": tflops / peak,
                      "peak_source": f"{src} bf16_tflops (burst; the clock record is beside it)",
                      "frac_of_sustained_peak": tflops / peak_sus, "traffic": None},
-        "gpu_launches": 3 * args.steps, "clocks": clk.summary(),
+        "gpu_launches": 2 * args.steps, "clocks": clk.summary(),
     }
     print(json.dumps(line), flush=True)
     return 0

@@ -8,12 +8,13 @@
 // no part (dQ = 0) and pad keys get dK = dV = 0.
 //
 // Kernels, in launch order:
-//   bwd_rowdot_kernel     D per packed row (fp32; bf16 runs bwd_rowstat_tc_kernel,
-//                         which also writes -LSE * log2(e) and -D per row of whole
-//                         tiles, as the tensor-core dK/dV kernel reads them).
+//   bwd_rowdot_kernel     D per packed row.
 //   bwd_transpose_kernel  for each key tile, the ascending list of query tiles
 //                         that keep it (one warp per key tile: a binary search
 //                         in every query tile's sorted list, ballots, prefix).
+//                         (bf16: both in bwd_prepare_tc_kernel, with -LSE * log2(e)
+//                         and -D per row of whole tiles, as the tensor-core dK/dV
+//                         units read them.)
 //   bwd_dq_kernel         one warp per query row, walking its tile's kept list
 //                         (fp32; bf16 runs bwd_tc_kernel on the tensor cores).
 //   bwd_dkdv_kernel       one warp per key row, walking the transposed list
@@ -21,7 +22,7 @@
 // The SIMT kernels (fp32 storage) use fp32 arithmetic, one lane per four
 // channels; for bf16 every product runs on the tensor cores
 // (ssta_attn_bwd_tc.cu).
-#include "ssta_internal.h"
+#include "ssta_bwd_lists.cuh"
 
 #include <cuda_bf16.h>
 
@@ -121,41 +122,10 @@ bwd_rowdot_kernel(Geom g, int64_t bh0, const T* __restrict__ o, const T* __restr
   }
 }
 
-// For key tile j of head bh: tidx[bh][j][0..tcnt) = query tiles i (ascending) whose
-// kept list holds j.  Lists are ascending (as ssta_build_block_mask writes them).
 __global__ void __launch_bounds__(kBwdWarps * 32)
 bwd_transpose_kernel(Geom g, const int32_t* __restrict__ kv_idx, const int32_t* __restrict__ kv_cnt,
                      int32_t* __restrict__ tidx, int32_t* __restrict__ tcnt, int32_t* __restrict__ status) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kBwdWarps + (threadIdx.x >> 5);   // bh * NQ + j
-  if (w >= (int64_t)g.B * g.H * g.NQ) return;
-  const int64_t bh = w / g.NQ;
-  const int j = (int)(w - bh * g.NQ);
-  int32_t* out = tidx + w * g.NQ;
-  int n = 0;
-  for (int i0 = 0; i0 < g.NQ; i0 += 32) {
-    const int i = i0 + lane;
-    bool keeps = false;
-    if (i < g.NQ) {
-      const int64_t lr = bh * g.NQ + i;
-      int c = kv_cnt[lr];
-      if (c < 0 || c > g.max_kept) {
-        atomicExch(status, (int)SSTA_ERR_DEVICE_BOUNDS);
-        c = c < 0 ? 0 : g.max_kept;
-      }
-      const int32_t* l = kv_idx + lr * g.max_kept;
-      int lo = 0, hi = c;                      // first entry >= j
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (l[mid] < j) lo = mid + 1; else hi = mid;
-      }
-      keeps = lo < c && l[lo] == j;
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, keeps);
-    if (keeps) out[n + __popc(m & ((1u << lane) - 1u))] = i;
-    n += __popc(m);
-  }
-  if (lane == 0) tcnt[w] = n;
+  transpose_lists(g, (int64_t)blockIdx.x * kBwdWarps + (threadIdx.x >> 5), kv_idx, kv_cnt, tidx, tcnt, status);
 }
 
 template <typename T>
@@ -249,7 +219,7 @@ constexpr bool kTensorCores<__nv_bfloat16> = true;
 
 template <typename T>
 cudaError_t launch_bwd_typed(const Geom& g, const void* q, const void* k, const void* v, const void* o,
-                             const ssta_checkpoint* o_saved, const float* lse, const void* dO, const int32_t* kv_idx,
+                             const ssta_checkpoint* saved, const float* lse, const void* dO, const int32_t* kv_idx,
                              const int32_t* kv_cnt, void* dq, void* dk, void* dv, const BwdWorkspace& ws, uint8_t* base,
                              cudaStream_t s) {
   const int64_t rows = (int64_t)g.B * g.H * g.Lq, tiles = (int64_t)g.B * g.H * g.NQ;
@@ -264,8 +234,12 @@ cudaError_t launch_bwd_typed(const Geom& g, const void* q, const void* k, const 
   const T* tO = static_cast<const T*>(dO);
   float* nl2 = reinterpret_cast<float*>(base + ws.nl2);
   float* nd = reinterpret_cast<float*>(base + ws.nd);
-  if constexpr (kTensorCores<T>) {
-    cudaError_t e = launch_attention_bwd_rowstat_tc(g, o, o_saved, dO, lse, Dv, nl2, nd, s);
+  if constexpr (kTensorCores<T>) {   // bf16: the API guarantees N % 128 == 0
+    cudaError_t e = launch_attention_bwd_prepare_tc(g, o, saved, const_cast<void*>(q), const_cast<void*>(k),
+                                                          const_cast<void*>(v), dO, lse, kv_idx, kv_cnt, Dv, nl2, nd, tidx,
+                                                          tcnt, status, s);
+    if (e != cudaSuccess) return e;
+    e = launch_attention_bwd_tc(g, q, k, v, dO, lse, Dv, nl2, nd, kv_idx, kv_cnt, tidx, tcnt, dq, dk, dv, status, s);
     if (e != cudaSuccess) return e;
   } else {
     const int64_t rows_per_block = (int64_t)kBwdWarps * kRowdotRows, BH = (int64_t)g.B * g.H;
@@ -273,13 +247,7 @@ cudaError_t launch_bwd_typed(const Geom& g, const void* q, const void* k, const 
       const dim3 grid((unsigned)((g.Lq + rows_per_block - 1) / rows_per_block), (unsigned)std::min<int64_t>(BH - bh0, 65535));
       bwd_rowdot_kernel<T><<<grid, kBwdWarps * 32, 0, s>>>(g, bh0, static_cast<const T*>(o), tO, Dv);
     }
-  }
-  bwd_transpose_kernel<<<tb, kBwdWarps * 32, 0, s>>>(g, kv_idx, kv_cnt, tidx, tcnt, status);
-  if constexpr (kTensorCores<T>) {   // bf16: the API guarantees N % 128 == 0
-    const cudaError_t e = launch_attention_bwd_tc(g, q, k, v, dO, lse, Dv, nl2, nd, kv_idx, kv_cnt, tidx, tcnt, dq, dk,
-                                                  dv, status, s);
-    if (e != cudaSuccess) return e;
-  } else {
+    bwd_transpose_kernel<<<tb, kBwdWarps * 32, 0, s>>>(g, kv_idx, kv_cnt, tidx, tcnt, status);
     bwd_dq_kernel<T><<<rb, kBwdWarps * 32, 0, s>>>(g, tq, tk, tv, tO, lse, Dv, kv_idx, kv_cnt, static_cast<T*>(dq),
                                                    status);
     bwd_dkdv_kernel<T><<<rb, kBwdWarps * 32, 0, s>>>(g, tq, tk, tv, tO, lse, Dv, tidx, tcnt, static_cast<T*>(dk),
@@ -305,14 +273,14 @@ BwdWorkspace bwd_workspace_layout(const Geom& g) {
 }
 
 cudaError_t launch_attention_bwd(const Geom& g, const void* q, const void* k, const void* v, const void* o,
-                                 const ssta_checkpoint* o_saved, const float* lse, const void* dO,
+                                 const ssta_checkpoint* saved, const float* lse, const void* dO,
                                  const int32_t* kv_idx, const int32_t* kv_cnt, void* dq, void* dk, void* dv,
                                  void* workspace, cudaStream_t s) {
   if ((int64_t)g.B * g.H == 0) return cudaSuccess;
   const BwdWorkspace ws = bwd_workspace_layout(g);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   if (g.dtype == SSTA_BF16)
-    return launch_bwd_typed<__nv_bfloat16>(g, q, k, v, o, o_saved, lse, dO, kv_idx, kv_cnt, dq, dk, dv, ws, base, s);
+    return launch_bwd_typed<__nv_bfloat16>(g, q, k, v, o, saved, lse, dO, kv_idx, kv_cnt, dq, dk, dv, ws, base, s);
   return launch_bwd_typed<float>(g, q, k, v, o, nullptr, lse, dO, kv_idx, kv_cnt, dq, dk, dv, ws, base, s);
 }
 

@@ -21,7 +21,8 @@
 // dS(j-1) is written: the next chunk's S and dP run during this chunk's
 // exponentials.  dS is overwritten only after the previous dQ product finished.
 // Every wait is bounded (ssta_wait.cuh), as in the forward kernel.
-#include "ssta_rows.cuh"
+#include "ssta_bwd_lists.cuh"
+#include "ssta_checkpoint.cuh"
 #include "ssta_tc_common.cuh"
 
 #include <algorithm>
@@ -327,26 +328,28 @@ dq_unit(int64_t u, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
 namespace {
 
 // Row statistics for the tensor-core kernels, per packed row of whole tiles:
-// D = rowsum(dO * O) (rows < Lq), and the values the dK/dV kernel adds,
+// What the main kernel needs first, in one grid of 256-thread blocks (three small launches
+// one behind the other took 15 of the 106 us of a three-head problem): the row statistics,
+// the transposed lists and, with checkpoints, the values of q, k and v.
+//
+// Row statistics: D = rowsum(dO * O) (rows < Lq), and the values the dK/dV units add,
 // -LSE * log2(e) and -D (-inf and 0 for pad rows and rows without a kept key).
 // 16 lanes per row (16-byte loads of 8 bf16 channels), 8 rows per warp with every
 // load issued before the first sum; row validity from the tile tables, so no lane
-// divides by the grid extents; grid.y is the head.
+// divides by the grid extents.
+// CODES: O is an 8-bit checkpoint, decoded here (half the bytes of a bf16 O, and no
+// pass that writes its values out).
 constexpr int kRsWarps = 8;
 constexpr int kRsRows = 8;   // rows per warp
 
-// CODES: O is an 8-bit checkpoint, decoded here (half the bytes of a bf16 O, and no
-// pass that writes its values out).
 template <bool CODES>
-__global__ void __launch_bounds__(kRsWarps * 32)
-bwd_rowstat_tc_kernel(const Geom g, const __grid_constant__ ChunkTables tb, int64_t bh0,
-                      const __nv_bfloat16* __restrict__ o, const ssta_checkpoint oc,
-                      const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse, float* __restrict__ Dv,
-                      float* __restrict__ nl2, float* __restrict__ nd) {
+__device__ __forceinline__ void row_statistics(const Geom& g, const ChunkTables& tb, int64_t bh, int64_t block,
+                                               const __nv_bfloat16* __restrict__ o, const ssta_checkpoint& oc,
+                                               const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse,
+                                               float* __restrict__ Dv, float* __restrict__ nl2, float* __restrict__ nd) {
   const int lane = threadIdx.x & 31, sub = lane >> 4, part = lane & 15;
-  const int64_t bh = bh0 + blockIdx.y;
   const int64_t Lp = (int64_t)g.NQ * g.N;
-  const int64_t r0 = ((int64_t)blockIdx.x * kRsWarps + (threadIdx.x >> 5)) * kRsRows;
+  const int64_t r0 = (block * kRsWarps + (threadIdx.x >> 5)) * kRsRows;
   int4 va[kRsRows / 2], vb[kRsRows / 2];   // CODES: va.x and va.y hold the codes, va.z the exponent byte
   bool valid[kRsRows / 2];
 #pragma unroll
@@ -407,24 +410,66 @@ bwd_rowstat_tc_kernel(const Geom g, const __grid_constant__ ChunkTables tb, int6
   }
 }
 
+template <bool CODES>
+__global__ void __launch_bounds__(kRsWarps * 32)
+bwd_prepare_tc_kernel(const __grid_constant__ Geom g, const __grid_constant__ ChunkTables tb, unsigned head_blocks,
+                      unsigned stat_blocks, unsigned load_blocks, const __nv_bfloat16* __restrict__ o,
+                      const ssta_checkpoint oc, const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse,
+                      float* __restrict__ Dv, float* __restrict__ nl2, float* __restrict__ nd,
+                      const __grid_constant__ ckpt::Params values, const int32_t* __restrict__ kv_idx,
+                      const int32_t* __restrict__ kv_cnt, int32_t* __restrict__ tidx, int32_t* __restrict__ tcnt,
+                      int32_t* __restrict__ status) {
+  unsigned b = blockIdx.x;
+  if (b < stat_blocks) {
+    row_statistics<CODES>(g, tb, b / head_blocks, b % head_blocks, o, oc, dO, lse, Dv, nl2, nd);
+    return;
+  }
+  b -= stat_blocks;
+  if constexpr (CODES) {
+    if (b < 3 * load_blocks) {
+      ckpt::load_block<__nv_bfloat16>(values, (int)(b / load_blocks), b % load_blocks);
+      return;
+    }
+    b -= 3 * load_blocks;
+  }
+  transpose_lists(g, (int64_t)b * kRsWarps + (threadIdx.x >> 5), kv_idx, kv_cnt, tidx, tcnt, status);
+}
+
 }  // namespace
 
-cudaError_t launch_attention_bwd_rowstat_tc(const Geom& g, const void* o, const ssta_checkpoint* o_saved,
-                                            const void* dO, const float* lse, float* Dv, float* nl2, float* nd,
-                                            cudaStream_t s) {
-  const int64_t BH = (int64_t)g.B * g.H;
+cudaError_t launch_attention_bwd_prepare_tc(const Geom& g, const void* o, const ssta_checkpoint* saved, void* q, void* k,
+                                            void* v, const void* dO, const float* lse, const int32_t* kv_idx,
+                                            const int32_t* kv_cnt, float* Dv, float* nl2, float* nd, int32_t* tidx,
+                                            int32_t* tcnt, int32_t* status, cudaStream_t s) {
+  static_assert(ckpt::kThreads == kRsWarps * 32, "one block size for all parts");
+  const int64_t BH = (int64_t)g.B * g.H, tiles = BH * g.NQ;
   const int64_t Lp = (int64_t)g.NQ * g.N, rows_per_block = (int64_t)kRsWarps * kRsRows;
+  const int64_t head_blocks = (Lp + rows_per_block - 1) / rows_per_block, stat_blocks = BH * head_blocks;
+  const int64_t list_blocks = (tiles + kRsWarps - 1) / kRsWarps;
   const ChunkTables tb = make_chunk_tables(g);
-  for (int64_t bh0 = 0; bh0 < BH; bh0 += 65535) {   // grid.y holds at most 65535 heads
-    const dim3 grid((unsigned)((Lp + rows_per_block - 1) / rows_per_block), (unsigned)std::min<int64_t>(BH - bh0, 65535));
-    if (o_saved != nullptr)
-      bwd_rowstat_tc_kernel<true><<<grid, kRsWarps * 32, 0, s>>>(g, tb, bh0, nullptr, *o_saved,
-                                                                 static_cast<const __nv_bfloat16*>(dO), lse, Dv, nl2, nd);
-    else
-      bwd_rowstat_tc_kernel<false><<<grid, kRsWarps * 32, 0, s>>>(g, tb, bh0, static_cast<const __nv_bfloat16*>(o),
-                                                                  ssta_checkpoint{}, static_cast<const __nv_bfloat16*>(dO),
-                                                                  lse, Dv, nl2, nd);
+  ckpt::Params values{};
+  int64_t load_blocks = 0;
+  if (saved != nullptr) {
+    values = ckpt::params(BH * g.Lq, g.D, saved[0].format);
+    void* const to[3] = {q, k, v};
+    for (int i = 0; i < 3; ++i) {
+      values.in[i] = saved[i].codes;
+      values.exps[i] = saved[i].exponents;
+      values.out[i] = to[i];
+    }
+    load_blocks = ckpt::blocks_for(values.groups);
   }
+  const int64_t blocks = stat_blocks + 3 * load_blocks + list_blocks;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const __nv_bfloat16* dOb = static_cast<const __nv_bfloat16*>(dO);
+  if (saved != nullptr)
+    bwd_prepare_tc_kernel<true><<<(unsigned)blocks, kRsWarps * 32, 0, s>>>(
+        g, tb, (unsigned)head_blocks, (unsigned)stat_blocks, (unsigned)load_blocks, nullptr, saved[3], dOb, lse, Dv, nl2, nd,
+        values, kv_idx, kv_cnt, tidx, tcnt, status);
+  else
+    bwd_prepare_tc_kernel<false><<<(unsigned)blocks, kRsWarps * 32, 0, s>>>(
+        g, tb, (unsigned)head_blocks, (unsigned)stat_blocks, 0u, static_cast<const __nv_bfloat16*>(o), ssta_checkpoint{}, dOb,
+        lse, Dv, nl2, nd, values, kv_idx, kv_cnt, tidx, tcnt, status);
   return cudaGetLastError();
 }
 

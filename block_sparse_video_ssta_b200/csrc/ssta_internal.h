@@ -95,16 +95,19 @@ cudaError_t launch_select_and_list(const Geom& g, const float* scores, int32_t* 
 cudaError_t launch_attention_f32(const Geom& g, const float* qp, const float* kp, const float* vp,
                                  const int32_t* kv_idx, const int32_t* kv_cnt, float* o, float* lse,
                                  int32_t* status, cudaStream_t s);
-// O from `o`, or, when o_saved is given (bf16 only), from its 8-bit checkpoint.
+// saved != NULL (bf16 only): the checkpoints of q, k, v and O; q, k and v then are room for
+// their values and `o` is not read.
 cudaError_t launch_attention_bwd(const Geom& g, const void* q, const void* k, const void* v, const void* o,
-                                 const ssta_checkpoint* o_saved, const float* lse, const void* dO,
+                                 const ssta_checkpoint* saved, const float* lse, const void* dO,
                                  const int32_t* kv_idx, const int32_t* kv_cnt, void* dq, void* dk, void* dv,
                                  void* workspace, cudaStream_t s);
-// bf16, N % 128 == 0: row statistics for the tensor-core kernel, and dQ, dK and dV in one
-// grid (Dv = rowsum(dO * O); tidx/tcnt: the transposed lists).
-cudaError_t launch_attention_bwd_rowstat_tc(const Geom& g, const void* o, const ssta_checkpoint* o_saved,
-                                            const void* dO, const float* lse, float* Dv, float* nl2, float* nd,
-                                            cudaStream_t s);
+// bf16, N % 128 == 0: what the tensor-core kernel needs first (row statistics, transposed
+// lists, the checkpoints' values), and dQ, dK and dV in one grid (Dv = rowsum(dO * O);
+// tidx/tcnt: the transposed lists).
+cudaError_t launch_attention_bwd_prepare_tc(const Geom& g, const void* o, const ssta_checkpoint* saved, void* q, void* k,
+                                            void* v, const void* dO, const float* lse, const int32_t* kv_idx,
+                                            const int32_t* kv_cnt, float* Dv, float* nl2, float* nd, int32_t* tidx,
+                                            int32_t* tcnt, int32_t* status, cudaStream_t s);
 cudaError_t launch_attention_bwd_tc(const Geom& g, const void* q, const void* k, const void* v, const void* dO,
                                     const float* lse, const float* Dv, const float* nl2, const float* nd,
                                     const int32_t* kv_idx, const int32_t* kv_cnt, const int32_t* tidx,

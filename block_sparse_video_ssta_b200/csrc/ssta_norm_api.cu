@@ -299,17 +299,19 @@ ssta_status ssta_attention_bwd_checkpoint(const ssta_desc* desc, const ssta_chec
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(int32_t), s) != cudaSuccess) return SSTA_ERR_LAUNCH;
   if (empty) return SSTA_OK;
-  // The tensor-core kernels take their operands by TMA, so the values of q, k and v are
-  // written out once; O is only read for its row dot with dO, which decodes it (bf16), or
-  // is written to dq's place, which the dQ kernel overwrites last (fp32).
+  // The tensor-core kernel takes its operands by TMA, so the values of q, k and v are
+  // written out once (bf16: with the row statistics, where O is decoded too; fp32: O's
+  // values go to dq's place, which the dQ kernel overwrites last).
   uint8_t* values = static_cast<uint8_t*>(workspace) + bwd_workspace_layout(g).total;
   void* x[3] = {values, values + packed_bytes(g), values + 2 * packed_bytes(g)};
   const bool bf16 = g.dtype == SSTA_BF16;
-  const int64_t rows = (int64_t)g.B * g.H * g.Lq;
-  cudaError_t e = launch_checkpoint_load(rows, g.D, bf16, c, x, 3, s);
-  if (e == cudaSuccess && !bf16) e = launch_checkpoint_load(rows, g.D, false, &c[3], &dq_packed, 1, s);
-  if (e != cudaSuccess) return from_cuda(e);
-  return from_cuda(launch_attention_bwd(g, x[0], x[1], x[2], bf16 ? nullptr : dq_packed, bf16 ? &c[3] : nullptr, lse,
+  if (!bf16) {
+    const int64_t rows = (int64_t)g.B * g.H * g.Lq;
+    cudaError_t e = launch_checkpoint_load(rows, g.D, false, c, x, 3, s);
+    if (e == cudaSuccess) e = launch_checkpoint_load(rows, g.D, false, &c[3], &dq_packed, 1, s);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  return from_cuda(launch_attention_bwd(g, x[0], x[1], x[2], bf16 ? nullptr : dq_packed, bf16 ? c : nullptr, lse,
                                         do_packed, kv_idx, kv_cnt, dq_packed, dk_packed, dv_packed, workspace, s));
 }
 
