@@ -92,7 +92,7 @@ __device__ __forceinline__ bool row_valid(const Geom& g, int t, const TileValid&
 }
 
 // D = rowsum(dO * O) per packed row for the fp32 kernels (bf16 uses
-// bwd_rowstat_tc_kernel): each lane reads 16 bytes (4 channels), 32 lanes per row,
+// bwd_prepare_tc_kernel): each lane reads 16 bytes (4 channels), 32 lanes per row,
 // four rows per warp with every load issued before the first sum; grid.y is the head.
 constexpr int kRowdotRows = 4;
 template <typename T>
