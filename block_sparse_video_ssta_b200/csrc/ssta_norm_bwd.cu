@@ -198,12 +198,18 @@ struct Kernel {
   static constexpr int kStageBytes = NV * U * kVecBytes;
   static constexpr int kScales = SRC ? MAXT * NV * kVec / kGroup : 0;   // group scales of a row
   static constexpr int kTable = kWindow * ((int)sizeof(RowScalars) + (POST ? 2 : 1) * kScales * 4);
+  // With two vectors per thread and a gated residual the products of the parameter vectors do
+  // not fit in registers beside the sums: each thread keeps its own in shared memory (100 M
+  // bf16 elements in rows of 8,192 channels: 208 us instead of 255 us with the spills).  Dense
+  // fp32 rows need that memory for copies in flight.
+  static constexpr bool kShared = NV > 1 && POST && !(sizeof(T) == 4 && SRC == 0);
+  static constexpr int kVectors = kShared ? NV * 2 * kVec * 4 * MAXT : 0;
   // copies in flight: up to four times U rows, as far as shared memory goes (two blocks of
   // 256 threads, or one larger one, per SM)
-  static constexpr int kFit = ((MAXT <= 256 ? 112 : 224) * 1024 - kTable) / kStageBytes;
+  static constexpr int kFit = ((MAXT <= 256 ? 112 : 224) * 1024 - kTable - kVectors) / kStageBytes;
   static constexpr int kStages = kFit < 1 ? 1 : kFit < 4 ? kFit : 4;
   static constexpr int kSumBytes = kSums * NV * kVec * 4 * MAXT;
-  static constexpr int kSmem = kTable + (kStages * kStageBytes > kSumBytes ? kStages * kStageBytes : kSumBytes);
+  static constexpr int kSmem = kTable + kVectors + (kStages * kStageBytes > kSumBytes ? kStages * kStageBytes : kSumBytes);
 };
 
 template <typename T, int SRC, int POST, bool HALF, int NV, int U, int MAXT>
@@ -215,7 +221,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
   RowScalars* const table = reinterpret_cast<RowScalars*>(smem);
   float* const scales_r = reinterpret_cast<float*>(smem + kWindow * sizeof(RowScalars));
   float* const scales_y = scales_r + kWindow * K::kScales;
-  uint8_t* const stage = smem + K::kTable;
+  float4* const vectors = reinterpret_cast<float4*>(smem + K::kTable);
+  uint8_t* const stage = smem + K::kTable + K::kVectors;
   const NormBwdArgs& a = p.a;
   const int warps = p.row_threads >> 5;
   const int slot = HALF ? threadIdx.x >> 4 : threadIdx.x / p.row_threads;
@@ -321,6 +328,24 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
     products(float());
   else
     products(__nv_bfloat16());
+  auto vector_place = [&](int k, int i) { return vectors + (k * NV + i) * 2 * MAXT + threadIdx.x; };
+  if constexpr (K::kShared) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const Raw<float> r = pack(k ? gp[i] : gw[i], 0.f);
+        vector_place(k, i)[0] = r.a;
+        vector_place(k, i)[MAXT] = r.b;
+      }
+    }
+  }
+  auto product = [&](int k, int i) {   // 0: of the norm, 1: of the gate and the post norm
+    if constexpr (K::kShared)
+      return unpack(Raw<float>{vector_place(k, i)[0], vector_place(k, i)[MAXT]});
+    else
+      return k ? gp[POST ? i : 0] : gw[i];
+  };
   V8 s1[NV], s2[NV], s3[POST ? NV : 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i) s1[i] = s2[i] = fill(0.f);
@@ -358,7 +383,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
         rh[u][i] = kept(u, i, K::kR, scales_r, rs.x, rs.y);
         s1[i] = add(s1[i], dn);
         s2[i] = fma(dn, rh[u][i], s2[i]);
-        g[u][i] = mul(dn, gw[i]);
+        g[u][i] = mul(dn, product(0, i));
         m1[u] += sum(g[u][i]);
         m2[u] += dot(g[u][i], rh[u][i]);
       }
@@ -384,7 +409,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_bwd_kernel(con
         if constexpr (POST) {
           yh[u][i] = kept(u, i, K::kY, scales_y, sc.prstd, sc.pshift);
           s3[i] = fma(dR[u][i], yh[u][i], s3[i]);
-          dR[u][i] = mul(dR[u][i], gp[i]);
+          dR[u][i] = mul(dR[u][i], product(1, i));
           if constexpr (POST == kGate) {
             if (live && in[i]) store8(dy + off, dR[u][i]);
           } else {
