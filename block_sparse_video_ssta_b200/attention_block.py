@@ -106,9 +106,11 @@ def _tokens(desc, video, text, out=None):
     return out.flatten(2)
 
 
+@torch.no_grad()
 def ssta_block_forward(desc: Desc, x, mod, w: BlockWeights, checkpoint=None, stream=None):
-    """Returns (r, n2 [B, L, C], saved).  ``checkpoint``: None (keep what the backward reads as it is), "int8" or
-    "e4m3"."""
+    """Returns (r, n2 [B, L, C], saved).  ``checkpoint``: None (keep what the backward reads as it is, x by
+    reference), "int8" or "e4m3".  The gradients are ssta_block_backward's: nothing is recorded for torch's autograd,
+    whatever requires a gradient."""
     nd = _check(desc, x, mod, w)
     with _on(stream, _device(x, "x")):
         shift, scale, gate, shift2, scale2 = mod.unbind(1)
@@ -124,6 +126,7 @@ def ssta_block_forward(desc: Desc, x, mod, w: BlockWeights, checkpoint=None, str
     return f.r, f.n, saved
 
 
+@torch.no_grad()
 def ssta_block_backward(desc: Desc, saved: BlockSaved, w: BlockWeights, dr, dn2, stream=None) -> BlockGrads:
     """Gradients from those of r and n2 [B, L, C]."""
     mod = saved.mod

@@ -214,6 +214,21 @@ def test_block_captured_and_on_a_stream(cuda_ok):
             assert torch.equal(a, b)
 
 
+def test_parameters_that_require_gradients(cuda_ok):
+    """nn.Parameters and leaves as arguments: the same bytes, and nothing recorded by autograd."""
+    w = with_overrides(si.get_workload("small_bf16"), H=1, T=4, Y=8, X=16)
+    d = S.desc_from(w)
+    x, mod, p, dr, dn = block_inputs(w)
+    param = torch.nn.Parameter
+    q = BlockWeights(param(p.qkv), param(p.out), param(p.q_norm), param(p.k_norm))
+    for checkpoint in (None, "int8"):
+        a, b = (ssta_block_forward(d, xx, mod, pp, checkpoint) for xx, pp in ((x, p), (x.clone().requires_grad_(), q)))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and not b[0].requires_grad and not b[1].requires_grad
+        ga, gb = ssta_block_backward(d, a[2], p, dr, dn), ssta_block_backward(d, b[2], q, dr, dn)
+        for n in ("dx", "dmod", "dqkv", "dout", "dq_norm", "dk_norm"):
+            assert torch.equal(getattr(ga, n), getattr(gb, n)) and not getattr(gb, n).requires_grad, n
+
+
 def test_checkpoints_halve_what_is_kept(cuda_ok):
     w = with_overrides(si.get_workload("small_bf16"), H=2, T=8, Y=16, X=24)
     d = S.desc_from(w)
