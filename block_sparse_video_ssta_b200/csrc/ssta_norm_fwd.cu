@@ -4,17 +4,17 @@
 // Every row is read once, held in registers, and written once: the statistics (mean, then
 // the mean square of the differences, both fp32) are sums over registers and warp
 // shuffles, so the kernel moves 2 (norm) or 4 (residual) elements per channel and is
-// bound by HBM.  A row belongs to one warp up to 1,024 channels (half a warp up to 128)
-// and to 2, 4 or 8 warps above, which exchange their partial sums through shared memory;
-// a thread holds four vectors of 8 channels per array, of one wide row or of several
-// narrow ones, which keeps enough loads in flight without any staging.  Weights and modulation rows are shared by many rows and come from L1/L2.
-// An 8-bit checkpoint of an input or of r is written in the same pass from the registers.
+// bound by HBM.  A row belongs to one warp up to 1,024 channels (half a warp up to 128; two
+// warps from 769 on where a residual adds a second array) and to 2, 4 or 8 warps above,
+// which exchange their partial sums through shared memory; a thread holds two to four
+// vectors of 8 channels per array, of one wide row or of several narrow ones, which keeps
+// enough loads in flight without any staging.  Weights and modulation rows are shared by
+// many rows and come from L1/L2.  An 8-bit checkpoint of an input or of r is written in the
+// same pass from the registers.
 // Measured, of the measured copy rate: residual and norm of 111,600 x 2,048 bf16 295 us
 // (0.94), RMS norm of 1,785,600 x 128 bf16 152 us (0.93), 97,656 x 1,024 fp32 0.98.
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
-
-#include <algorithm>
 
 namespace ssta {
 namespace {
