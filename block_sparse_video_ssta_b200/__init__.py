@@ -313,7 +313,8 @@ def ssta_forward(desc: Desc, q, k, v, q_text=None, k_text=None, v_text=None, str
     ``q_weight``, ``k_weight`` [D] (bf16 or f32): RMS-normalise every head's q and k (video
     and text) with these weights first.  ``checkpoint``: None, "int8" or "e4m3"; with a
     format, what ssta_backward reads is kept as 8-bit checkpoints and the packed tensors
-    are not returned (qp, kp, vp and O_packed are None).  ``saved`` in the result is
+    are not returned (qp, kp, vp and O_packed are None).  O and LSE do not depend on it:
+    they are those of the tensors as they came.  ``saved`` in the result is
     ssta_backward's argument.
     """
     if q_weight is None and k_weight is None and checkpoint is None:
@@ -340,6 +341,7 @@ def ssta_forward(desc: Desc, q, k, v, q_text=None, k_text=None, v_text=None, str
         if checkpoint is not None:
             names = ("qp", "kp", "vp", "O_packed")
             r["saved"].q, r["saved"].k, r["saved"].v, r["saved"].o = (ssta_checkpoint_save(r[n], checkpoint) for n in names)
+            r["saved"].lse = None
             r.update(dict.fromkeys(names))
         return r
 
@@ -354,13 +356,14 @@ def _attend(desc, qp, kp, vp, stream, tile_scores):
 
 @dataclass
 class SstaSaved:
-    """What ssta_backward reads: the packed q, k, v and O (tensors, or Checkpoints), LSE, the kept lists, and for q
-    and k the head norm's (descriptor, input, rstd, weight), None where there is no norm."""
+    """What ssta_backward reads: the packed q, k, v and O (tensors, or Checkpoints), LSE (None with Checkpoints, whose
+    values have another one), the kept lists, and for q and k the head norm's (descriptor, input, rstd, weight), None
+    where there is no norm.  As a Checkpoint, O serves what follows the attention (its projection's gradient)."""
     q: object
     k: object
     v: object
     o: object
-    lse: torch.Tensor
+    lse: torch.Tensor | None
     kv_idx: torch.Tensor
     kv_cnt: torch.Tensor
     norms: tuple = (None, None)
@@ -370,16 +373,26 @@ def ssta_backward(desc: Desc, saved: SstaSaved, dO, dO_text=None, stream=None):
     """The whole SSTA backward, from the gradients of ssta_forward's O [B,H,T,Y,X,D] and O_text [B,H,L,D].
 
     ``saved``: ``ssta_forward(...)["saved"]``.  The kept lists are constants: no gradient
-    passes through the selection.  Returns a dict with dq, dk, dv (raster), dq_text, dk_text,
-    dv_text (None without text), dq_weight, dk_weight ([D] float32, None without head norms)
-    and the attention backward's workspace (ssta_read_device_status)."""
+    passes through the selection.  From checkpoints the attention runs once more, over their
+    values, and the gradients are those of that attention.  Returns a dict with dq, dk, dv
+    (raster), dq_text, dk_text, dv_text (None without text), dq_weight, dk_weight ([D]
+    float32, None without head norms) and a workspace with the device status of everything
+    that ran (ssta_read_device_status)."""
     with _on(stream, _device(dO, "dO")):
         do = ssta_tile_reorder(desc, dO, dO_text)
-        rest = (saved.lse, do, saved.kv_idx, saved.kv_cnt)
-        if isinstance(saved.q, Checkpoint):
-            *grads, ws = ssta_attention_bwd_checkpoint(desc, saved.q, saved.k, saved.v, saved.o, *rest)
-        else:
-            *grads, ws = ssta_attention_bwd(desc, saved.q, saved.k, saved.v, saved.o, saved.lse, *rest[1:])
+        lists = (saved.kv_idx, saved.kv_cnt)
+        q, k, v, o, lse, ws_attn = saved.q, saved.k, saved.v, saved.o, saved.lse, None
+        if isinstance(q, Checkpoint):
+            # P = exp(S - LSE) is a softmax, and D the mean of dP under it, only with the LSE and the O of the very
+            # q, k and v that S and dP are formed from: with those of the unquantised tensors the rows of P sum to
+            # exp(LSE' - LSE), which grows with the logits
+            q, k, v = (ssta_checkpoint_load(c) for c in (q, k, v))
+            o, lse, ws_attn = ssta_attention_fwd(desc, q, k, v, *lists)
+        *grads, ws = ssta_attention_bwd(desc, q, k, v, o, lse, do, *lists)
+        del q, k, v, o
+        if ws_attn is not None:   # one status word for both: the larger code
+            status, of_fwd = (w[:4].view(torch.int32) for w in (ws, ws_attn))
+            torch.maximum(status, of_fwd, out=status)
         out = dict(workspace=ws)
         for name, g, norm in zip(("q", "k", "v"), grads, saved.norms + (None,)):
             if norm is not None:

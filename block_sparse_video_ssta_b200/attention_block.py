@@ -14,7 +14,8 @@ text tokens.  The modulation is [B, 5, C]: shift, scale, gate, shift2, scale2.  
 projections are library GEMMs; everything else runs in the library's kernels and layout
 copies.  With a ``checkpoint`` format everything the backward needs is kept in 8 bits
 (9.1 bytes per token and channel, against 18 in bf16): x, the packed q, k, v and O, q
-and k before their norms, y and r.
+and k before their norms, y and r.  The attention's gradients are then those at the values
+of q, k and v (ssta_backward), the output projection's is that of the kept O.
 """
 from __future__ import annotations
 

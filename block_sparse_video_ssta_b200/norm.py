@@ -500,7 +500,8 @@ def ssta_checkpoint_load(ckpt: Checkpoint, x=None, stream=None):
 def ssta_attention_bwd_checkpoint(desc: Desc, q, k, v, o, lse, do_packed, kv_idx, kv_cnt, dq=None, dk=None, dv=None,
                                   workspace=None, stream=None):
     """Backward of Step 4 from 8-bit checkpoints of the packed q, k, v and O (one format): returns
-    (dq, dk, dv [B,H,Lq,D], workspace)."""
+    (dq, dk, dv [B,H,Lq,D], workspace).  ``lse`` and ``o`` are those of ssta_attention_fwd over the checkpoints' values
+    of q, k and v, not over what these were before (ssta_backward computes both anew)."""
     p = ssta_plan(desc)
     dt = _torch_dtype(desc)
     dev = _device(do_packed, "do_packed")

@@ -402,8 +402,10 @@ ssta_status ssta_checkpoint_load(int64_t rows, int C, int dtype, const ssta_chec
 /*
  * ssta_attention_bwd_checkpoint — ssta_attention_bwd with q, k, v and O kept in 8
  * bits: checkpoints of the packed tensors ([B*H*Lq, 128], one format for all
- * four).  The formulas of ssta_attention_bwd at the checkpoints' values; lse is the
- * forward's.  workspace >= ssta_attention_bwd_checkpoint_workspace (which is
+ * four).  The formulas of ssta_attention_bwd at the checkpoints' values.  lse and O are
+ * those of ssta_attention_fwd over these values of q, k and v: with the LSE of other q and
+ * k (the tensors before they were rounded, say) the rows of P = exp(S - LSE) sum to
+ * exp(LSE(values) - LSE), which is unbounded and grows with the logits.  workspace >= ssta_attention_bwd_checkpoint_workspace (which is
  * info.bwd_workspace_bytes and room for the values of q, k and v; status word
  * first).  Otherwise as ssta_attention_bwd.
  */
