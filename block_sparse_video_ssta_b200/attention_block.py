@@ -19,7 +19,8 @@ of q, k and v (ssta_backward), the output projection's is that of the kept O.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+import weakref
+from dataclasses import dataclass, field
 
 import torch
 
@@ -42,7 +43,8 @@ class BlockWeights:
 
 @dataclass
 class BlockSaved:
-    """What ssta_block_backward reads; x, y and r are tensors or Checkpoints."""
+    """What ssta_block_backward reads; x, y and r are tensors or Checkpoints.  x, mod, the head norms' weights and,
+    without checkpoints, r are the caller's own tensors: they stay unchanged until the backward."""
     x: object
     y: object
     r: object
@@ -52,6 +54,18 @@ class BlockSaved:
     rstd2: torch.Tensor
     mod: torch.Tensor
     attention: SstaSaved
+    # r as the forward returned it, and its version (a next residual may be written over it)
+    _returned: tuple | None = field(default=None, repr=False, compare=False)
+
+    def __getstate__(self):   # a copy has an r of its own
+        return {**self.__dict__, "_returned": None}
+
+    def check_unchanged(self):
+        """Raises where the r that the caller was given has been written since the forward."""
+        r, version = self._returned or (None, None)
+        if r is not None and r() is self.r and self.r._version != version:
+            raise ValueError("r was written after ssta_block_forward returned it, and the backward reads it: write the "
+                             "next residual elsewhere, or keep a checkpoint")
 
 
 @dataclass
@@ -109,8 +123,9 @@ def _tokens(desc, video, text, out=None):
 
 @torch.no_grad()
 def ssta_block_forward(desc: Desc, x, mod, w: BlockWeights, checkpoint=None, stream=None):
-    """Returns (r, n2 [B, L, C], saved).  ``checkpoint``: None (keep what the backward reads as it is, x by
-    reference), "int8" or "e4m3".  The gradients are ssta_block_backward's: nothing is recorded for torch's autograd,
+    """Returns (r, n2 [B, L, C], saved).  ``checkpoint``: None (keep what the backward reads as it is, x and the
+    returned r by reference: ssta_block_backward refuses an r that was written since), "int8" or "e4m3" (mod and the
+    head norms' weights are kept by reference all the same).  The gradients are ssta_block_backward's: nothing is recorded for torch's autograd,
     whatever requires a gradient."""
     nd = _check(desc, x, mod, w)
     with _on(stream, _device(x, "x")):
@@ -124,6 +139,8 @@ def ssta_block_forward(desc: Desc, x, mod, w: BlockWeights, checkpoint=None, str
         y = torch.matmul(_tokens(desc, a["O"], a["O_text"]), w.out.t())
         f = ssta_residual_norm_fwd(nd, x, y, None, gate, None, scale2, shift2, save_y=checkpoint, save_r=checkpoint)
         saved = BlockSaved(x_saved or x, f.saved_y or y, f.saved_r or f.r, mean, rstd, f.mean, f.rstd, mod, a["saved"])
+        if checkpoint is None and not f.r.is_inference():   # inference tensors have no version
+            saved._returned = (weakref.ref(f.r), f.r._version)
     return f.r, f.n, saved
 
 
@@ -132,6 +149,7 @@ def ssta_block_backward(desc: Desc, saved: BlockSaved, w: BlockWeights, dr, dn2,
     """Gradients from those of r and n2 [B, L, C]."""
     mod = saved.mod
     nd = _check(desc, dr, mod, w, dn2=dn2)
+    saved.check_unchanged()
     with _on(stream, _device(dr, "dr")):
         shift, scale, gate, _, scale2 = mod.unbind(1)
         g2 = ssta_residual_norm_bwd(nd, dr, dn2, saved.r, saved.y, saved.mean2, saved.rstd2, None, None, None, gate, None,

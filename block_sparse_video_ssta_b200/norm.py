@@ -11,7 +11,8 @@ Activations are dense [..., C] tensors of ``rows`` rows; weights [C]; modulation
 ``mod.chunk(6, dim=-1)`` of a [G, 6 C] tensor can be passed as it is.
 
 A call given a ``stream`` runs and allocates on that stream: order its inputs before it
-and its outputs' readers behind it as for any work on that stream.
+and its outputs' readers behind it as for any work on that stream.  A tensor that the
+caller passes to be written counts as changed in place, as after torch's own operations.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ import functools
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import SSTA_BF16, SSTA_F32, Desc, _D, _P, _check, _ptr, _torch_dtype, _workspace, lib, ssta_plan
 
@@ -237,12 +239,13 @@ def _device(t, name):
 
 class _Args:
     """Checks one call's tensors against its descriptor and returns their addresses."""
-    __slots__ = ("desc", "dev", "index", "rows", "C", "n", "dtype", "param", "groups")
+    __slots__ = ("desc", "dev", "index", "rows", "C", "n", "dtype", "param", "groups", "given")
 
     def __init__(self, desc: NormDesc, dev):
         self.desc, self.dev, self.index = desc, dev, dev.index
         self.rows, self.C = desc.rows, desc.C
         self.n = self.rows * self.C
+        self.given = []   # the caller's tensors that the call writes
         self.dtype = torch.bfloat16 if desc.dtype == SSTA_BF16 else torch.float32
         self.param = torch.bfloat16 if desc.param_dtype == SSTA_BF16 else torch.float32
         m = desc.mod_rows
@@ -330,6 +333,7 @@ class _Args:
         if t is None:
             t = torch.empty_like(like)
             return t, t.data_ptr()
+        self.given.append(t)
         return t, self.act(t, name)
 
     def out_stat(self, t, name, wanted, like=None):
@@ -338,6 +342,7 @@ class _Args:
                 return None, None
             t = torch.empty_like(like) if like is not None else torch.empty(self.rows, dtype=torch.float32, device=self.dev)
             return t, t.data_ptr()
+        self.given.append(t)
         return t, self.stat(t, name)
 
     def out_grad(self, t, name, wanted, groups=None, like=None):
@@ -348,6 +353,7 @@ class _Args:
             shape = (self.C,) if groups is None else (groups, self.C)
             t = torch.empty_like(like) if like is not None else torch.empty(shape, dtype=torch.float32, device=self.dev)
             return t, t.data_ptr()
+        self.given.append(t)
         return t, self.grad(t, name, groups or 1)
 
     def workspace(self, t):
@@ -355,6 +361,14 @@ class _Args:
             t = _workspace(_bwd_bytes(self.rows, self.C, self.desc.mod_rows), self.dev)
             return t, t.data_ptr()
         return t, self._dense(t, "workspace", torch.uint8, t.numel(), 0)
+
+
+    def check(self, code, where):
+        """Raises on a non-zero status; otherwise the caller's tensors count as written, as after torch's own
+        in-place operations (an address does not tell torch)."""
+        _check(code, where)
+        if self.given:
+            increment_version(self.given)
 
 
 def _ref(ckpt):
@@ -375,7 +389,7 @@ def ssta_norm_fwd(desc: NormDesc, x, weight=None, scale=None, shift=None, y=None
         mean, pm = a.out_stat(mean, "mean", stats and desc.norm == 1)
         rstd, pr = a.out_stat(rstd, "rstd", stats, mean)
         saved = a.save(save, x, "save")
-        _check(lib.ssta_norm_fwd(
+        a.check(lib.ssta_norm_fwd(
             ctypes.byref(desc), px, a.weight(weight, "weight"), a.mod(scale, "scale"), a.mod(shift, "shift"),
             py, pm, pr, _ref(saved), _current(dev)), "ssta_norm_fwd")
     return y, mean, rstd, saved
@@ -396,7 +410,7 @@ def ssta_norm_bwd(desc: NormDesc, dy, x, mean, rstd, weight=None, scale=None, dr
         dscale, pds = a.out_grad(dscale, "dscale", scale is not None, a.groups)
         dshift, pdt = a.out_grad(dshift, "dshift", scale is not None if want_dshift is None else want_dshift, a.groups, dscale)
         workspace, pw = a.workspace(workspace)
-        _check(lib.ssta_norm_bwd(
+        a.check(lib.ssta_norm_bwd(
             ctypes.byref(desc), pdy, px, cx, a.stat(mean, "mean"), a.stat(rstd, "rstd"), a.weight(weight, "weight"),
             a.mod(scale, "scale"), a.act(dres, "dres"), pdx, pdw, pds, pdt, pw, workspace.numel(), _current(dev)),
             "ssta_norm_bwd")
@@ -420,7 +434,7 @@ def ssta_residual_norm_fwd(desc: NormDesc, x, y, post_weight=None, gate=None, we
         rs, p_rs = a.out_stat(None, "rstd", stats and desc.norm != 0, pr)
         m, p_m = a.out_stat(None, "mean", stats and desc.norm == 1, rs)
         cy, cr = a.save(save_y, y, "save_y"), a.save(save_r, x, "save_r")
-        _check(lib.ssta_residual_norm_fwd(
+        a.check(lib.ssta_residual_norm_fwd(
             ctypes.byref(desc), px, py, a.weight(post_weight, "post_weight"), a.mod(gate, "gate"),
             a.weight(weight, "weight"), a.mod(scale, "scale"), a.mod(shift, "shift"), p_r, p_n, p_pm, p_pr, p_m, p_rs,
             _ref(cy), _ref(cr), _current(dev)), "ssta_residual_norm_fwd")
@@ -451,7 +465,7 @@ def ssta_residual_norm_bwd(desc: NormDesc, dr, dn, r=None, y=None, mean=None, rs
         dshift, pdt = a.out_grad(dshift, "dshift", normed and (scale is not None if want_dshift is None else want_dshift),
                                  a.groups, dscale)
         workspace, pw = a.workspace(workspace)
-        _check(lib.ssta_residual_norm_bwd(
+        a.check(lib.ssta_residual_norm_bwd(
             ctypes.byref(desc), pdr, pdn, pr_, cr, py, cy, a.stat(post_mean, "post_mean"), a.stat(post_rstd, "post_rstd"),
             a.stat(mean, "mean"), a.stat(rstd, "rstd"), a.weight(post_weight, "post_weight"), a.mod(gate, "gate"),
             a.weight(weight, "weight"), a.mod(scale, "scale"), pdx, pdy, pdp, pdg, pdw, pds, pdt, pw, workspace.numel(),
@@ -483,8 +497,9 @@ def ssta_checkpoint_load(ckpt: Checkpoint, x=None, stream=None):
     dev = _device(ckpt, "ckpt")
     if not isinstance(ckpt, Checkpoint):
         raise ValueError("ckpt must be a Checkpoint")
+    given = x is not None
     with _on(stream, dev):
-        if x is None:
+        if not given:
             x = torch.empty_like(ckpt._codes, dtype=ckpt._dtype)
             px = x.data_ptr()
         else:
@@ -494,6 +509,8 @@ def ssta_checkpoint_load(ckpt: Checkpoint, x=None, stream=None):
         C = x.shape[-1]
         _check(lib.ssta_checkpoint_load(x.numel() // max(C, 1), C, _VALUE_DTYPES[ckpt._dtype], ckpt._ref(), px,
                                         _current(dev)), "ssta_checkpoint_load")
+        if given:
+            increment_version(x)
     return x
 
 
