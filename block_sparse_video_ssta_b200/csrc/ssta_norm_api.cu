@@ -222,8 +222,9 @@ ssta_status ssta_residual_norm_bwd(const ssta_norm_desc* desc, const void* dr, c
   a.rstd = rstd;
   a.post_weight = post_weight;
   a.gate = gate;
-  a.weight = weight;
-  a.scale = scale;
+  // (without dn the norm's vectors would multiply zeros, and an infinity or a NaN among them make a NaN)
+  a.weight = use_r ? weight : nullptr;
+  a.scale = use_r ? scale : nullptr;
   a.dx = dx;
   a.dy = dy;
   a.dpost_weight = dpost_weight;
