@@ -7,10 +7,12 @@
 // (int8: |x| * 2^(127 - E) < 127.5; e4m3: <= 448).  Scaling by a power of two is exact,
 // so a code is the nearest one to x with ties to even and nothing else is rounded, and a
 // code times its scale (7 or 4 significant bits) is exact in bf16: what the tensor cores
-// multiply is what the checkpoint holds.  A finer scale would halve int8's step at most
-// and put a rounding behind every read.  A group with an infinity, a NaN or a magnitude
-// whose nearest value would be 2^128 gets E = 255 and reads as NaN throughout, so an
-// overflow stays visible in the gradients.
+// multiply is what the checkpoint holds.  (E never goes below 1.  The steps of e4m3 are then
+// 2^-135, or 2^-134 with E = 2, below bf16's smallest number 2^-133; the codes of a bf16
+// tensor do not use them, since its numbers are multiples of 2^-133.)  A finer scale would
+// halve int8's step at most and put a rounding behind every read.  A group with an infinity,
+// a NaN or a magnitude whose nearest value would be 2^128 gets E = 255 and reads as NaN
+// throughout, so an overflow is not silently clipped.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -110,10 +112,6 @@ __device__ __forceinline__ Raw<float> pack(const V8& v, float) {
 }
 template <typename T> __device__ __forceinline__ V8 load8(const T* p) { return unpack(load_raw(p)); }
 template <typename T> __device__ __forceinline__ void store8(T* p, const V8& v) { store_raw(p, pack(v, T())); }
-// Eight elements of a parameter vector of either type (is_f32 is the same for a whole launch).
-__device__ __forceinline__ V8 load_param8(const void* p, int64_t i, bool is_f32) {
-  return is_f32 ? load8(static_cast<const float*>(p) + i) : load8(static_cast<const __nv_bfloat16*>(p) + i);
-}
 
 __device__ __forceinline__ V8 mul(const V8& a, const V8& b) {
   return {f2_mul(a.p[0], b.p[0]), f2_mul(a.p[1], b.p[1]), f2_mul(a.p[2], b.p[2]), f2_mul(a.p[3], b.p[3])};

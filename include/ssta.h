@@ -206,9 +206,10 @@ ssta_status ssta_attention_fwd(const ssta_desc* desc, const void* q_packed, cons
  *   workspace >= info.bwd_workspace_bytes (status word, per-row D, per-row -LSE and -D
  *   over whole tiles for the bf16 kernels, and for every key tile the list of query
  *   tiles keeping it).
- * bf16 (N % 128 == 0 required, as for ssta_attention_fwd): tcgen05 tensor-core
- * kernels, one for dQ over each query tile's kept list, one for dK and dV over the
- * query tiles keeping each key tile.  fp32: SIMT kernels with fp32 arithmetic.
+ * bf16 (N % 128 == 0 required, as for ssta_attention_fwd): one tcgen05 tensor-core
+ * kernel, whose blocks form dK and dV over the query tiles keeping each key tile, or dQ
+ * over each query tile's kept list; P and dS enter their products rounded to bf16.
+ * fp32: SIMT kernels with fp32 arithmetic.
  * Returns SSTA_ERR_UNSUPPORTED for bf16 with N % 128 != 0, SSTA_ERR_WORKSPACE for a
  * missing or short workspace, SSTA_ERR_ALIGNMENT for a workspace not 256-byte aligned
  * or a tensor not 16-byte aligned, SSTA_ERR_INVALID_ARG for a NULL tensor.
@@ -293,19 +294,23 @@ typedef struct {
 typedef struct {
   int64_t groups;               /* G */
   int exponents_per_row;        /* ceil(C / 128) */
-  size_t bwd_workspace_bytes;   /* workspace for ssta_norm_bwd and ssta_residual_norm_bwd */
+  size_t bwd_workspace_bytes;   /* workspace for ssta_norm_bwd and ssta_residual_norm_bwd: 12 bytes per channel
+                                   and run of rows, a few hundred runs, or one per group where there are more
+                                   groups (mod_rows = 1: 12 bytes per element) */
 } ssta_norm_plan_info;
 
 /*
  * An activation kept in 8 bits.  128 consecutive channels of a row (fewer at its
  * end) share one exponent byte E: value = code * 2^(E - 127), with E the smallest
  * in [1, 254] that gives the group's largest magnitude a code.  Codes are rounded
- * to nearest, ties to even; every value is exact in bf16.  A group that holds an
- * infinity, a NaN or a magnitude whose nearest value would be 2^128 has E = 255 and
- * all its values read as NaN.  Largest error of
- * a value: max|group| / 127.5 (int8; half a step, and the step is at most twice
- * the finest one), or |x| * 2^-4 (e4m3; below 2^-14 of the group's largest
- * magnitude the steps are equal).
+ * to nearest, ties to even.  A group that holds an infinity, a NaN or a magnitude
+ * whose nearest value would be 2^128 has E = 255 and all its values read as NaN.
+ * Largest error of a value: half a step, 2^(E - 128) (int8), which is at most
+ * max|group| / 127.5 unless E is held at 1 (max|group| below 63.75 * 2^-126); or
+ * |x| * 2^-4, and 2^(E - 137) below 2^(E - 133), where the steps are equal (e4m3).
+ * Every int8 value is exact in bf16, and so is every e4m3 value of a bf16 tensor; of an
+ * fp32 tensor, e4m3 values with E = 1 or 2 go down to 2^-135, below bf16's smallest
+ * number 2^-133, and reading them as bf16 rounds.
  */
 typedef enum { SSTA_INT8 = 0, SSTA_E4M3 = 1 } ssta_code_format;
 typedef struct {
@@ -327,7 +332,8 @@ ssta_status ssta_norm_plan(const ssta_norm_desc* desc, ssta_norm_plan_info* info
  *   x [rows, C] (read), y [rows, C] (written; may be x), mean, rstd [rows]
  *   (written when non-NULL; mean must be NULL for the RMS norm), x_save (NULL, or
  *   a checkpoint of x to write in the same pass).
- * desc->norm must not be SSTA_NORM_NONE; post_norm and res_scale are ignored.
+ * desc->norm must not be SSTA_NORM_NONE; post_norm and res_scale are not used (but have
+ * to be valid, as in every call).
  */
 ssta_status ssta_norm_fwd(const ssta_norm_desc* desc, const void* x, const void* weight, const void* scale,
                           const void* shift, void* y, float* mean, float* rstd, const ssta_checkpoint* x_save,
