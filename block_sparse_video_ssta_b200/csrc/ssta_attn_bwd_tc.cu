@@ -20,6 +20,11 @@
 // dQ += dS(j-1) K(j-1) (A = dS from tensor memory, B = K read MN-major) once
 // dS(j-1) is written: the next chunk's S and dP run during this chunk's
 // exponentials.  dS is overwritten only after the previous dQ product finished.
+// Rounding: S, dP, P and dS are fp32 up to the products dS K (here) and P^T dO, dS^T Q
+// (below), whose operands the bf16 MMA takes as bf16: half a step each, 2^-8 relative at
+// most.  The gradients are then off by 2.4e-3 (relative 2-norm against 64 bits) where their
+// own storage in bf16 costs 1.7e-3.  As tf32 the products would run at half the rate, from
+// twice the shared and tensor memory, which are full.
 // Every wait is bounded (ssta_wait.cuh), as in the forward kernel.
 #include "ssta_bwd_lists.cuh"
 #include "ssta_checkpoint.cuh"
@@ -327,13 +332,13 @@ dq_unit(int64_t u, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
 
 namespace {
 
-// Row statistics for the tensor-core kernels, per packed row of whole tiles:
 // What the main kernel needs first, in one grid of 256-thread blocks (three small launches
 // one behind the other took 15 of the 106 us of a three-head problem): the row statistics,
 // the transposed lists and, with checkpoints, the values of q, k and v.
 //
-// Row statistics: D = rowsum(dO * O) (rows < Lq), and the values the dK/dV units add,
-// -LSE * log2(e) and -D (-inf and 0 for pad rows and rows without a kept key).
+// Row statistics, per packed row of whole tiles: D = rowsum(dO * O) (rows < Lq), and the
+// values the dK/dV units add, -LSE * log2(e) and -D (-inf and 0 for pad rows and rows
+// without a kept key).
 // 16 lanes per row (16-byte loads of 8 bf16 channels), 8 rows per warp with every
 // load issued before the first sum; row validity from the tile tables, so no lane
 // divides by the grid extents.
@@ -481,7 +486,7 @@ cudaError_t launch_attention_bwd_prepare_tc(const Geom& g, const void* o, const 
 //              columns 64 (w / 4) .. +63 of each step, in two phases: P^T from
 //              S^T (bf16, written over the S^T columns the warp read), then dS^T
 //              from dP^T and P (bf16, likewise over dP^T); the per-query -LSE
-//              (log2 units) and -D are the rows the row-dot kernel wrote, staged
+//              (log2 units) and -D are the rows of the row statistics, staged
 //              in shared memory with dO; epilogue (the warps of query half 0
 //              write dV, those of half 1 dK)
 //   warp  8    producer: K and V of the block once; per step Q (3-stage ring)

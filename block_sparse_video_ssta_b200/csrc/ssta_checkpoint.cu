@@ -2,7 +2,8 @@
 // Elementwise over groups of 128 channels, one half-warp per group (8 channels per lane:
 // a group's largest magnitude is three register steps and four shuffles), bound by HBM:
 // 3 bytes per bf16 element and 1/128 byte of exponents in either direction.  219,600 x
-// 2,048 bf16 there and back: 400 us, 6.8 TB/s, 1.03 of the measured copy rate.
+// 2,048 bf16 there and back: 408-423 us back to back, 0.97-1.01 of the measured copy rate (400
+// us with L2 flushed between passes).
 #include "ssta_checkpoint.cuh"
 
 namespace ssta {

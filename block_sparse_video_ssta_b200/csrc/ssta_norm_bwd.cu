@@ -21,9 +21,14 @@
 // What bounds it: HBM, once the instructions fit.  A thread handles two rows at a time and
 // works on pairs of channels; the row sums of both rows share one butterfly, in which a
 // lane gives away the sums that it need not finish (6 shuffles for four sums instead of
-// 20).  219,600 x 2,048 bf16 (gradients of r and n in, of x and y out): 725 us from int8
-// checkpoints, 6.2 TB/s, 0.95 of the measured copy rate; 920 us dense (0.89).  One row at a
-// time in scalar arithmetic took 1,165 and 986 us.
+// 20).  219,600 x 2,048 bf16 (gradients of r and n in, of x and y out), passes back to back:
+// 754-813 us from int8 checkpoints, 0.85-0.91 of the measured copy rate (the power cap decides
+// which; 725 us, 0.95, with L2 flushed between passes), 967 us dense, 0.85 (910 us, 0.90).
+// One row at a time in scalar arithmetic took 1,165 and 986 us with pauses.  Rows of 128
+// channels (heads): 1,785,600 of them take 262 us from dense rows (0.80) and from int8 (0.67)
+// alike, so what bounds them is not the bytes.  A modulation row per token makes every run one
+// row: 6.1 ms dense for 219,600 x 2,048 (0.32, fp32 gradients of the modulation included), and
+// the runs' sums take 5.4 GB.
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
 

@@ -11,8 +11,10 @@
 // enough loads in flight without any staging.  Weights and modulation rows are shared by
 // many rows and come from L1/L2.  An 8-bit checkpoint of an input or of r is written in the
 // same pass from the registers.
-// Measured, of the measured copy rate: residual and norm of 111,600 x 2,048 bf16 295 us
-// (0.94), RMS norm of 1,785,600 x 128 bf16 152 us (0.93), 97,656 x 1,024 fp32 0.98.
+// Measured, passes back to back (of the measured copy rate; in parentheses with L2 flushed
+// between passes, which leaves the GPU pauses): residual and norm of 111,600 x 2,048 bf16
+// 309 us, 0.90 (295 us, 0.94), with two int8 saves 444 us, 0.78; RMS norm of 1,785,600 x 128
+// bf16 154-164 us, 0.86-0.90 (152 us, 0.93); 97,656 x 1,024 fp32 (0.98).
 #include "ssta_norm.h"
 #include "ssta_rows.cuh"
 
@@ -106,9 +108,10 @@ __device__ __forceinline__ V8 param8(const void* v, int64_t at, bool in, float o
 }
 
 // NV vectors per lane and row, U rows per thread, LPR lanes and WPR warps per row; POST:
-// with a gated residual.  Blocks per SM: four without a residual (64 registers; three and
-// 76 take 162 us instead of 152 us for 1,785,600 rows of 128 bf16 channels, and so do two
-// rows per thread with five blocks), three with one (80 registers), two where more is held.
+// with a gated residual.  Blocks per SM: four without a residual (64 registers, for which the
+// kernels with four vectors per thread up to 512 channels store 24 to 80 bytes per thread to
+// local memory; three and 76 registers take 162 us instead of 152 us for 1,785,600 rows of
+// 128 bf16 channels, and so do two rows per thread with five blocks), three with one (80 registers), two where more is held.
 template <typename T, typename P, int NV, int U, int LPR, int WPR, bool POST>
 __global__ void __launch_bounds__(kFwdThreads, !POST ? 4 : sizeof(T) == 2 && WPR > 1 ? 3 : 2) norm_fwd_kernel(const __grid_constant__ FwdParams p) {
   constexpr int kRowThreads = LPR * WPR, kSlots = kFwdThreads / kRowThreads;
